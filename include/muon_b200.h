@@ -201,7 +201,8 @@ muon_status_t muon_set_wait_timeout_us(int64_t us);
 /*
  * Per-kernel timing for diagnostics and benchmarks.  Between muon_profile_begin and
  * muon_profile_end every launch the library queues is bracketed by a pair of CUDA
- * events recorded on its own stream.  muon_profile_end waits for those events and
+ * events recorded on its own stream (the Muon step's kernels only: the layer entry points
+ * below are not timed).  muon_profile_end waits for those events and
  * returns, per kernel kind (MUON_KIND_*), the summed device time in milliseconds and
  * the number of launches.  Timing state is per process; calls are not thread safe
  * while a profile is open.
@@ -282,6 +283,145 @@ muon_status_t muon_adamw_step(const muon_adamw_tensor_t* tensors, int n, float l
 muon_status_t muon_newton_schulz_static(const muon_matrix_t* mats, int n, int ns_steps,
                                         const float* coeffs, float eps, int32_t* device_status,
                                         void* stream);
+
+/*
+ * Layers around the weight matrices, and their gradients.
+ *
+ * The steps above read gradients; these entry points run the layers whose parameters they
+ * update and write those gradients where the steps read them: fp32, strided like
+ * muon_matrix_t.grad, and optionally added to what the buffer holds (a further micro-batch).
+ * The pages describe the optimizer only; these are the textbook layers.
+ *
+ *   layer norm            y = (x - mean) rstd gain + bias,   rstd = 1 / sqrt(var + eps)
+ *   its gradients         h = (x - mean) rstd,  q = dy gain
+ *                         dx = rstd (q - avg(q) - h avg(q h)) + skip
+ *                         dgain (+)= sum over rows of dy h,  dbias (+)= sum over rows of dy
+ *   linear                z = x W^T + bias,  y = act(z) + residual
+ *   its gradients         dx = (dy W) act'(z_in) + skip,  dW (+)= dy^T x,  db (+)= sum of dy
+ *                         where z_in is what the activation that made x was applied to
+ *   activation            dz = dy act'(z)
+ *
+ * Matrices are row-major views (muon_view_t) of fp32 or bf16 elements, aligned to their
+ * element size; rows may be 0 (nothing but the parameter gradients is written then, as
+ * zeros, or left alone when accumulating).  Rows behind the last one and columns behind
+ * the last one of a strided view are neither read for their values nor written.
+ * A view that is written may overlap no other view of the call, except that y may be the
+ * residual and dx the skip gradient (same pointer, ld and dtype).
+ *
+ * Numerics: statistics, sums over rows and reductions of products are carried in fp32 (long
+ * reductions in pieces whose fp32 sums are added with rounding to nearest).  A bf16 operand
+ * of a product goes to the tensor cores as it is; an fp32 one as three bf16 terms that hold
+ * all of its 24 bits, so fp32 operands are not rounded (an infinite fp32 operand may give
+ * NaN where the exact result is infinite).  Each output is rounded once, to its dtype.
+ * Results do not depend on the order in which blocks run: no atomics on data.
+ *
+ * Execution, ownership and errors are those of the header's opening comment, with two
+ * differences: the workspace holds nothing between calls and needs no muon_workspace_init,
+ * and device-side waits that run out are recorded in one status word per device, read with
+ * muon_layers_status.  Calls that may overlap on the GPU need workspaces of their own.
+ */
+typedef enum {
+  MUON_ACT_NONE = 0,
+  MUON_ACT_RELU = 1,      /* max(z, 0) */
+  MUON_ACT_RELU2 = 2,     /* max(z, 0)^2 */
+  MUON_ACT_GELU = 3,      /* z Phi(z), Phi the normal distribution function */
+  MUON_ACT_GELU_TANH = 4, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  MUON_ACT_SILU = 5       /* z / (1 + exp(-z)) */
+} muon_act_t;
+
+/* A matrix (or, with ld ignored, a vector).  24 bytes.  data NULL: absent where allowed. */
+typedef struct {
+  void*   data;
+  int64_t ld;        /* row stride, elements; >= cols */
+  int32_t dtype;     /* muon_dtype_t */
+  int32_t reserved;  /* set to 0 */
+} muon_view_t;
+
+typedef struct {
+  muon_view_t x;      /* in  [rows x cols] */
+  muon_view_t gain;   /* in  [cols]; absent: 1 */
+  muon_view_t bias;   /* in  [cols]; absent: 0 */
+  muon_view_t y;      /* out [rows x cols], dtype of x */
+  float*  mean;       /* out [rows], may be NULL */
+  float*  rstd;       /* out [rows], may be NULL */
+  int64_t rows, cols;
+  float   eps;        /* >= 0, finite */
+  int32_t reserved;   /* set to 0 */
+} muon_layer_norm_t;
+
+muon_status_t muon_layer_norm(const muon_layer_norm_t* d, void* stream);
+
+typedef struct {
+  muon_view_t dy;      /* in  [rows x cols], dtype of x */
+  muon_view_t x;       /* in  [rows x cols] */
+  muon_view_t gain;    /* in  [cols]; absent: 1 */
+  muon_view_t skip;    /* in  [rows x cols], added to dx; absent: 0 */
+  muon_view_t dx;      /* out [rows x cols], dtype of x; absent: not computed */
+  const float* mean;   /* in  [rows] */
+  const float* rstd;   /* in  [rows] */
+  float*  dgain;       /* out [cols]; NULL: not computed */
+  float*  dbias;       /* out [cols]; NULL: not computed */
+  int64_t rows, cols;
+  int32_t accumulate;  /* 1: dgain and dbias are added to what their buffers hold */
+  int32_t reserved;    /* set to 0 */
+} muon_layer_norm_grad_t;
+
+/* Workspace bytes (may be 0) of muon_layer_norm_backward for these sizes. */
+muon_status_t muon_layer_norm_backward_workspace(const muon_layer_norm_grad_t* d, size_t* bytes);
+muon_status_t muon_layer_norm_backward(const muon_layer_norm_grad_t* d, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+typedef struct {
+  muon_view_t x;         /* in  [rows x in] */
+  muon_view_t w;         /* in  [out x in] */
+  muon_view_t bias;      /* in  [out]; absent: 0 */
+  muon_view_t residual;  /* in  [rows x out]; absent: 0 */
+  muon_view_t y;         /* out [rows x out] */
+  muon_view_t preact;    /* out [rows x out], receives z; absent: not stored */
+  int64_t rows, in, out;
+  int32_t act;           /* muon_act_t */
+  int32_t reserved;      /* set to 0 */
+} muon_linear_t;
+
+/* Workspace bytes (may be 0) of muon_linear for this descriptor on the current device. */
+muon_status_t muon_linear_workspace(const muon_linear_t* d, size_t* bytes);
+muon_status_t muon_linear(const muon_linear_t* d, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct {
+  muon_view_t dy;      /* in  [rows x out] */
+  muon_view_t x;       /* in  [rows x in]; needed for dw */
+  muon_view_t w;       /* in  [out x in]; needed for dx */
+  muon_view_t preact;  /* in  [rows x in]: z_in; needed for dx when in_act is not NONE */
+  muon_view_t skip;    /* in  [rows x in], added to dx; absent: 0 */
+  muon_view_t dx;      /* out [rows x in]; absent: not computed */
+  muon_view_t dw;      /* out [out x in], fp32; absent: not computed */
+  float*  db;          /* out [out]; NULL: not computed */
+  int64_t rows, in, out;
+  int32_t in_act;      /* muon_act_t: the activation that made x */
+  int32_t accumulate;  /* 1: dw and db are added to what their buffers hold */
+} muon_linear_grad_t;
+
+muon_status_t muon_linear_backward_workspace(const muon_linear_grad_t* d, size_t* bytes);
+muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+typedef struct {
+  muon_view_t dy;  /* in  [rows x cols] */
+  muon_view_t z;   /* in  [rows x cols] */
+  muon_view_t dz;  /* out [rows x cols], dtype of dy */
+  int64_t rows, cols;
+  int32_t act;       /* muon_act_t, not NONE */
+  int32_t reserved;  /* set to 0 */
+} muon_activation_grad_t;
+
+muon_status_t muon_activation_backward(const muon_activation_grad_t* d, void* stream);
+
+/*
+ * Waits for `stream`, then reads the current device's status word of the entry points above:
+ * MUON_OK, or MUON_ERR_TIMEOUT with the wait site in *where (may be NULL).  The first event
+ * wins and stays until a call with clear != 0 has read it.
+ */
+muon_status_t muon_layers_status(void* stream, int clear, int32_t* device_status, int32_t* where);
 
 #ifdef __cplusplus
 }

@@ -12,7 +12,8 @@ def __getattr__(name):
     # Lazy: importing the package (e.g. for the input generators) must not need torch/CUDA.
     if name in ("muon_step", "newton_schulz", "workspace_size", "scratch_view", "device_status",
                 "Workspace", "default_workspace", "QUINTIC", "quintic_table", "MuonError",
-                "MuonLibraryError"):
+                "MuonLibraryError", "layer_norm", "layer_norm_backward", "linear", "linear_backward",
+                "activation_backward", "layers_status"):
         from . import api
 
         return getattr(api, name)

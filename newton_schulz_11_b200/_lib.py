@@ -24,6 +24,7 @@ MUON_STATIC_SCRATCH_BYTES = 64 << 20
 
 MUON_F32 = 0
 MUON_BF16 = 1
+MUON_ACTS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}  # muon_act_t
 MUON_MAX_NS_STEPS = 16
 
 EXPORTS = (
@@ -41,6 +42,15 @@ EXPORTS = (
     "muon_profile_end",
     "muon_newton_schulz_static",
     "muon_adamw_step",
+    "muon_layer_norm",
+    "muon_layer_norm_backward",
+    "muon_layer_norm_backward_workspace",
+    "muon_linear",
+    "muon_linear_workspace",
+    "muon_linear_backward",
+    "muon_linear_backward_workspace",
+    "muon_activation_backward",
+    "muon_layers_status",
 )
 
 KIND_NAMES = ("momentum", "norm", "gram", "poly", "apply", "apply_last")
@@ -90,7 +100,72 @@ class MuonScratchView(ctypes.Structure):
     ]
 
 
+def _view(name):
+    """The four fields of a muon_view_t, flat, so that a descriptor is built in one call."""
+    return [(name + "_data", ctypes.c_void_p), (name + "_ld", ctypes.c_int64), (name + "_dtype", ctypes.c_int32),
+            (name + "_reserved", ctypes.c_int32)]
+
+
+class MuonLayerNorm(ctypes.Structure):
+    _fields_ = _view("x") + _view("gain") + _view("bias") + _view("y") + [
+        ("mean", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class MuonLayerNormGrad(ctypes.Structure):
+    _fields_ = _view("dy") + _view("x") + _view("gain") + _view("skip") + _view("dx") + [
+        ("mean", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("dgain", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("accumulate", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class MuonLinear(ctypes.Structure):
+    _fields_ = _view("x") + _view("w") + _view("bias") + _view("residual") + _view("y") + _view("preact") + [
+        ("rows", ctypes.c_int64),
+        ("in_features", ctypes.c_int64),
+        ("out_features", ctypes.c_int64),
+        ("act", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class MuonLinearGrad(ctypes.Structure):
+    _fields_ = _view("dy") + _view("x") + _view("w") + _view("preact") + _view("skip") + _view("dx") + _view("dw") + [
+        ("db", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("in_features", ctypes.c_int64),
+        ("out_features", ctypes.c_int64),
+        ("in_act", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+    ]
+
+
+class MuonActivationGrad(ctypes.Structure):
+    _fields_ = _view("dy") + _view("z") + _view("dz") + [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("act", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 assert ctypes.sizeof(MuonMatrix) == 80
+assert ctypes.sizeof(MuonLayerNorm) == 4 * 24 + 40
+assert ctypes.sizeof(MuonLayerNormGrad) == 5 * 24 + 56
+assert ctypes.sizeof(MuonLinear) == 6 * 24 + 32
+assert ctypes.sizeof(MuonLinearGrad) == 7 * 24 + 40
+assert ctypes.sizeof(MuonActivationGrad) == 3 * 24 + 24
 
 
 class MuonLibraryError(RuntimeError):
@@ -159,6 +234,20 @@ def lib() -> ctypes.CDLL:
         h.muon_newton_schulz_static.restype = ctypes.c_int
         h.muon_newton_schulz_static.argtypes = [P(MuonMatrix), ctypes.c_int, ctypes.c_int, P(ctypes.c_float),
                                                 ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]
+        for name, desc in (("muon_layer_norm_backward", MuonLayerNormGrad), ("muon_linear", MuonLinear),
+                           ("muon_linear_backward", MuonLinearGrad)):
+            f = getattr(h, name)
+            f.restype = ctypes.c_int
+            f.argtypes = [P(desc), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+            f = getattr(h, name + "_workspace")
+            f.restype = ctypes.c_int
+            f.argtypes = [P(desc), P(ctypes.c_size_t)]
+        for name, desc in (("muon_layer_norm", MuonLayerNorm), ("muon_activation_backward", MuonActivationGrad)):
+            f = getattr(h, name)
+            f.restype = ctypes.c_int
+            f.argtypes = [P(desc), ctypes.c_void_p]
+        h.muon_layers_status.restype = ctypes.c_int
+        h.muon_layers_status.argtypes = [ctypes.c_void_p, ctypes.c_int, P(ctypes.c_int32), P(ctypes.c_int32)]
         _lib = h
         return h
 

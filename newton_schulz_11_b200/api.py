@@ -12,6 +12,8 @@ import torch
 
 from . import _lib
 from ._lib import MUON_BF16, MUON_F32, MuonAdamwTensor, MuonError, MuonLibraryError, MuonMatrix, MuonScratchView, check, lib  # noqa: F401,E501
+from .layers import (activation_backward, layer_norm, layer_norm_backward, layers_status, linear,  # noqa: F401
+                     linear_backward)
 
 # "NanoGPT Speedrun" README, zeroth_power_via_newtonschulz5 listing: (a, b, c), 5 steps, eps.
 QUINTIC = (3.4445, -4.7750, 2.0315)

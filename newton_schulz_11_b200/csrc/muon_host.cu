@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "muon_b200.h"
+#include "muon_layers_host.h"
 #include "muon_params.h"
 
 namespace muon {
@@ -40,7 +41,6 @@ static_assert(sizeof(EwParams) < 32000, "kernel parameter block too large");
 constexpr size_t kHeaderBytes = 256;
 constexpr size_t kBufAlign = 1024;
 constexpr int64_t kChunkElems = 16384;
-constexpr int64_t kMaxSide = int64_t(1) << 24;
 constexpr int kStagedApplyMaxM = 1024;  // Gram side up to which the staged (64-deep) variants serve
 
 std::atomic<long long> g_timeout_us{2000000};
@@ -711,6 +711,14 @@ muon_status_t run(const muon_matrix_t* mats, int n, float lr, float beta, float 
 }
 
 }  // namespace
+
+// What the layer entry points share with the step: device facts and the wait budget.
+muon_status_t muon::layers_device(int* sms) {
+  int dev = 0;
+  return current_device(&dev, sms);
+}
+
+unsigned long long muon::layers_wait_ns() { return static_cast<unsigned long long>(g_timeout_us.load()) * 1000ull; }
 
 // ---------------------------------------------------------------- C ABI
 
