@@ -22,8 +22,9 @@ LIB = os.path.join(PKG, "libmuon_b200.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["muon_elementwise.cu", "muon_ns_gemm.cu", "muon_host.cu", "muon_adamw.cu",
-           "muon_norm.cu", "muon_linear.cu"]
-HEADERS = ["muon_device.cuh", "muon_params.h", "muon_layers.cuh", "muon_layers_host.h"]
+           "muon_norm.cu", "muon_linear.cu", "muon_product.cu"]
+HEADERS = ["muon_device.cuh", "muon_params.h", "muon_layers.cuh", "muon_layers_host.h",
+           "muon_product.h", "muon_epilogue.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC]

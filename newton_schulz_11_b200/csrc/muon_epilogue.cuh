@@ -1,0 +1,200 @@
+// The epilogue of the layer products: loads and stores of row segments, and the arithmetic.
+#pragma once
+
+#include "muon_device.cuh"
+#include "muon_layers.cuh"
+#include "muon_product.h"
+
+namespace muon {
+
+// NC (a multiple of 8) consecutive elements of a row, the first `valid` of them; the rest
+// are left at zero.  `off` is the element offset of the segment.
+template <int NC>
+__device__ __forceinline__ void load_segment(const EpiView& v, int64_t off, int valid, float (&x)[NC]) {
+  if (valid >= NC && v.vec) {
+    if (v.bf16) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(v.p) + off;
+      uint4 w[NC / 8];
+      if (NC % 16 == 0 && v.vec == 2) {
+#pragma unroll
+        for (int i = 0; i < NC / 16; ++i) ld_global_v8(p + 16 * i, w[2 * i], w[(2 * i + 1) % (NC / 8)]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+      }
+#pragma unroll
+      for (int i = 0; i < NC / 8; ++i) {
+        const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[8 * i + 2 * j] = __uint_as_float(q[j] << 16);
+          x[8 * i + 2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
+        }
+      }
+    } else {
+      const float* p = static_cast<const float*>(v.p) + off;
+      uint4 w[NC / 4];
+      if (v.vec == 2) {
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i) ld_global_v8(p + 8 * i, w[2 * i], w[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+      }
+#pragma unroll
+      for (int i = 0; i < NC / 4; ++i) {
+        x[4 * i] = __uint_as_float(w[i].x);
+        x[4 * i + 1] = __uint_as_float(w[i].y);
+        x[4 * i + 2] = __uint_as_float(w[i].z);
+        x[4 * i + 3] = __uint_as_float(w[i].w);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) x[j] = j < valid ? load_elem(v.p, off + j, v.bf16) : 0.f;
+  }
+}
+
+template <int NC>
+__device__ __forceinline__ void store_segment(const EpiView& v, int64_t off, int valid, const float (&x)[NC]) {
+  if (valid >= NC && v.vec) {
+    if (v.bf16) {
+      __nv_bfloat16* p = static_cast<__nv_bfloat16*>(v.p) + off;
+      uint4 w[NC / 8];
+#pragma unroll
+      for (int i = 0; i < NC / 8; ++i) {
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
+          q[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        w[i] = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+      if (NC % 16 == 0 && v.vec == 2) {
+#pragma unroll
+        for (int i = 0; i < NC / 16; ++i) st_global_v8(p + 16 * i, w[2 * i], w[(2 * i + 1) % (NC / 8)]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+      }
+    } else {
+      float* p = static_cast<float*>(v.p) + off;
+      uint4 w[NC / 4];
+#pragma unroll
+      for (int i = 0; i < NC / 4; ++i)
+        w[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+                          __float_as_uint(x[4 * i + 3]));
+      if (v.vec == 2) {
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i) st_global_v8(p + 8 * i, w[2 * i], w[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (j < valid) store_elem(v.p, off + j, v.bf16, x[j]);
+  }
+}
+
+// v = act(v) and v *= act'(t), the choice made once for the segment.
+template <int NC>
+__device__ __forceinline__ void apply_act(int act, float (&v)[NC]) {
+#define MUON_EACH(A)                                        \
+  case A:                                                   \
+    _Pragma("unroll") for (int j = 0; j < NC; ++j) v[j] = act_value(A, v[j]); \
+    break
+  switch (act) {
+    MUON_EACH(MUON_ACT_RELU);
+    MUON_EACH(MUON_ACT_RELU2);
+    MUON_EACH(MUON_ACT_GELU);
+    MUON_EACH(MUON_ACT_GELU_TANH);
+    MUON_EACH(MUON_ACT_SILU);
+    default: break;
+  }
+#undef MUON_EACH
+}
+
+template <int NC>
+__device__ __forceinline__ void apply_slope(int act, const float (&t)[NC], float (&v)[NC]) {
+#define MUON_EACH(A)                                        \
+  case A:                                                   \
+    _Pragma("unroll") for (int j = 0; j < NC; ++j) v[j] *= act_slope(A, t[j]); \
+    break
+  switch (act) {
+    MUON_EACH(MUON_ACT_RELU);
+    MUON_EACH(MUON_ACT_RELU2);
+    MUON_EACH(MUON_ACT_GELU);
+    MUON_EACH(MUON_ACT_GELU_TANH);
+    MUON_EACH(MUON_ACT_SILU);
+    default: break;
+  }
+#undef MUON_EACH
+}
+
+// Row m, columns [n, n + NC) of the output (n a multiple of 8), from the sums in v.
+template <int NC>
+__device__ __forceinline__ void finish_segment(const Epilogue& e, int64_t m, int64_t n, float (&v)[NC]) {
+  const int64_t left = e.cols - n;
+  if (m >= e.rows || left <= 0) return;
+  const int valid = left < NC ? static_cast<int>(left) : NC;
+  float t[NC];
+  if (e.bias.p != nullptr) {
+    load_segment<NC>(e.bias, n, valid, t);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) v[j] += t[j];
+  }
+  if (e.preact.p != nullptr) store_segment<NC>(e.preact, m * e.preact.ld + n, valid, v);
+  apply_act<NC>(e.act, v);
+  if (e.slope.p != nullptr) {
+    load_segment<NC>(e.slope, m * e.slope.ld + n, valid, t);
+    apply_slope<NC>(e.slope_act, t, v);
+  }
+  if (e.add.p != nullptr) {
+    load_segment<NC>(e.add, m * e.add.ld + n, valid, t);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) v[j] += t[j];
+  }
+  store_segment<NC>(e.out, m * e.out.ld + n, valid, v);
+}
+
+// Column n of rows [m, m + NC): neighbouring threads hold neighbouring columns.
+template <int NC>
+__device__ __forceinline__ void finish_column(const Epilogue& e, int64_t m, int64_t n, float (&v)[NC]) {
+  if (n >= e.cols) return;
+  const int64_t left = e.rows - m;
+  const int valid = left < NC ? static_cast<int>(left) : NC;
+  if (e.bias.p != nullptr) {
+    const float b = load_elem(e.bias.p, n, e.bias.bf16);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) v[j] += b;
+  }
+  if (e.preact.p != nullptr) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (j < valid) store_elem(e.preact.p, (m + j) * e.preact.ld + n, e.preact.bf16, v[j]);
+  }
+  apply_act<NC>(e.act, v);
+  float t[NC];
+  if (e.slope.p != nullptr) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      t[j] = j < valid ? load_elem(e.slope.p, (m + j) * e.slope.ld + n, e.slope.bf16) : 0.f;
+    apply_slope<NC>(e.slope_act, t, v);
+  }
+  if (e.add.p != nullptr) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      t[j] = j < valid ? load_elem(e.add.p, (m + j) * e.add.ld + n, e.add.bf16) : 0.f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) v[j] += t[j];
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+    if (j < valid) store_elem(e.out.p, (m + j) * e.out.ld + n, e.out.bf16, v[j]);
+}
+
+}  // namespace muon

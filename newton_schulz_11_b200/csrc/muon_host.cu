@@ -22,6 +22,7 @@
 #include "muon_b200.h"
 #include "muon_layers_host.h"
 #include "muon_params.h"
+#include "muon_product.h"
 
 namespace muon {
 cudaError_t launch_momentum(const EwParams& p, cudaStream_t stream);
@@ -719,6 +720,21 @@ muon_status_t muon::layers_device(int* sms) {
 }
 
 unsigned long long muon::layers_wait_ns() { return static_cast<unsigned long long>(g_timeout_us.load()) * 1000ull; }
+
+// 2-D bf16 map of a layer operand: boxes of 64 columns x box_rows rows, 128-byte swizzle,
+// zero fill outside the matrix.
+bool muon::encode_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                              int box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * 2)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(kBox), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // ---------------------------------------------------------------- C ABI
 

@@ -1,122 +1,105 @@
-// Linear layers and their gradients: the C ABI entry points, and the elementwise kernels.
+// Linear layers and their gradients: the C ABI entry points, the plan of each product, and
+// the elementwise kernels.
 //
-//   muon_linear            z = x W^T + bias,  y = act(z) + residual
-//   muon_linear_backward   dx = (dy W) act'(z_in) + skip,  dW (+)= dy^T x,  db (+)= sum of dy
+//   muon_linear               z = x W^T + bias,  y = act(z) + residual
+//   muon_linear_backward      dx = (dy W) act'(z_in) + skip,  dW (+)= dy^T x,  db (+)= sum of dy
 //   muon_activation_backward  dz = dy act'(z)
 //
-// All three products are D[M x N] = sum_k A(m, k) B(n, k) with operands that are contiguous
-// along k or along their own side, and one epilogue:
-//   v = sum + bias[n];  preact[m, n] = v;  v = act(v);  v *= act'(slope[m, n]);  v += add[m, n]
+// Workspace: the operands that the tensor cores cannot read in place (fp32 ones, as bf16
+// terms; bf16 ones whose rows are not 16-byte aligned, copied), the partial sums of split
+// reductions, and those of the bias gradient.  Nothing in it outlives the call.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 
-#include "muon_layers.cuh"
+#include "muon_epilogue.cuh"
 #include "muon_layers_host.h"
 
 namespace muon {
 
-struct ProductParams {
-  const void* a;
-  const void* b;
-  int64_t a_side, a_k, b_side, b_k;  // element strides
-  int64_t m, n, k;
-  int32_t a_bf16, b_bf16;
-  const void* bias;
-  void* preact;
-  const void* slope;
-  const void* add;
-  void* out;
-  int64_t ld_preact, ld_slope, ld_add, ld_out;
-  int32_t bias_bf16, preact_bf16, slope_bf16, add_bf16, out_bf16;
-  int32_t act, slope_act;
-};
-
-__global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ ProductParams p) {
-  __shared__ float sa[16][65], sb[16][65];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 64, n0 = static_cast<int64_t>(blockIdx.x) * 64;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < p.k; k0 += 16) {
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      const int ka = p.a_k == 1 ? (i & 15) : (i >> 6), ma = p.a_k == 1 ? (i >> 4) : (i & 63);
-      sa[ka][ma] = (m0 + ma < p.m && k0 + ka < p.k)
-                       ? load_elem(p.a, (m0 + ma) * p.a_side + (k0 + ka) * p.a_k, p.a_bf16) : 0.f;
-      const int kb = p.b_k == 1 ? (i & 15) : (i >> 6), nb = p.b_k == 1 ? (i >> 4) : (i & 63);
-      sb[kb][nb] = (n0 + nb < p.n && k0 + kb < p.k)
-                       ? load_elem(p.b, (n0 + nb) * p.b_side + (k0 + kb) * p.b_k, p.b_bf16) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[kk][ty + 16 * i], sb[kk][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= p.m || n >= p.n) continue;
-      float v = acc[i][j];
-      if (p.bias != nullptr) v += load_elem(p.bias, n, p.bias_bf16);
-      if (p.preact != nullptr) store_elem(p.preact, m * p.ld_preact + n, p.preact_bf16, v);
-      v = act_value(p.act, v);
-      if (p.slope != nullptr) v *= act_slope(p.slope_act, load_elem(p.slope, m * p.ld_slope + n, p.slope_bf16));
-      if (p.add != nullptr) v += load_elem(p.add, m * p.ld_add + n, p.add_bf16);
-      store_elem(p.out, m * p.ld_out + n, p.out_bf16, v);
-    }
-}
-
 struct ColumnSumParams {
   const void* dy;
   float* db;
-  int64_t rows, ld;
-  int32_t cols, bf16, accumulate;
+  float* partial;  // [slices][ld_partial]
+  int64_t rows, ld, ld_partial;
+  int32_t cols, bf16, vec, accumulate, slices;
 };
 
-// One warp-wide column group per block, all rows.
-__global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__ ColumnSumParams p) {
-  __shared__ float red[8][33];
+// Sums of columns over the rows: block (b, s) takes 256 columns, 8 a thread, and every
+// slices-th group of 8 rows.
+__global__ void __launch_bounds__(256) muon_column_sum_kernel(const __grid_constant__ ColumnSumParams p) {
+  __shared__ float red[8][256];
+  griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < p.cols)
-    for (int64_t r = w; r < p.rows; r += 8) s += load_elem(p.dy, r * p.ld + c, p.bf16);
-  red[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && c < p.cols) {
-    for (int k = 1; k < 8; ++k) s += red[k][lane];
-    p.db[c] = p.accumulate ? p.db[c] + s : s;
+  const int c = blockIdx.x * 256 + lane * 8;
+  const EpiView src{const_cast<void*>(p.dy), p.ld, p.bf16, p.vec};
+  float s[8] = {};
+  if (c < p.cols) {
+#pragma unroll 4
+    for (int64_t r = blockIdx.y * 8 + w; r < p.rows; r += int64_t(8) * gridDim.y) {
+      float x[8];
+      load_segment<8>(src, r * p.ld + c, p.cols - c, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += x[j];
+    }
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[w][lane * 8 + j] = s[j];
+  __syncthreads();
+  const int o = blockIdx.x * 256 + threadIdx.x;
+  if (o < p.cols) {
+    float t = red[0][threadIdx.x];
+    for (int k = 1; k < 8; ++k) t += red[k][threadIdx.x];
+    p.partial[blockIdx.y * p.ld_partial + o] = t;
+  }
+}
+
+__global__ void __launch_bounds__(256) muon_column_join_kernel(const __grid_constant__ ColumnSumParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= p.cols) return;
+  float t = 0.f;
+  for (int s = 0; s < p.slices; ++s) t += p.partial[s * p.ld_partial + c];
+  p.db[c] = p.accumulate ? p.db[c] + t : t;
 }
 
 struct ActGradParams {
-  const void* dy;
-  const void* z;
-  void* dz;
-  int64_t rows, cols, ld_dy, ld_z, ld_dz;
-  int32_t dy_bf16, z_bf16, act;
+  EpiView dy, z, dz;
+  int64_t rows, cols;
+  int32_t act;
 };
 
-__global__ void __launch_bounds__(256) activation_backward_kernel(const __grid_constant__ ActGradParams p) {
-  const int64_t per_row = (p.cols + 255) / 256;
-  for (int64_t b = blockIdx.x; b < p.rows * per_row; b += gridDim.x) {
-    const int64_t r = b / per_row, c = (b - r * per_row) * 256 + threadIdx.x;
-    if (c >= p.cols) continue;
-    const float g = load_elem(p.dy, r * p.ld_dy + c, p.dy_bf16);
-    store_elem(p.dz, r * p.ld_dz + c, p.dy_bf16, g * act_slope(p.act, load_elem(p.z, r * p.ld_z + c, p.z_bf16)));
+// Eight columns of a row per thread.
+__global__ void __launch_bounds__(256) muon_activation_backward_kernel(const __grid_constant__ ActGradParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t groups = (p.cols + 7) / 8;
+  const int64_t total = groups * p.rows;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t r = i / groups, c = (i - r * groups) * 8;
+    const int valid = p.cols - c < 8 ? static_cast<int>(p.cols - c) : 8;
+    float g[8], z[8];
+    load_segment<8>(p.dy, r * p.dy.ld + c, valid, g);
+    load_segment<8>(p.z, r * p.z.ld + c, valid, z);
+    apply_slope<8>(p.act, z, g);
+    store_segment<8>(p.dz, r * p.dz.ld + c, valid, g);
   }
 }
-
-__device__ int32_t g_layers_status[2];  // code, wait site
 
 }  // namespace muon
 
 namespace {
 using namespace muon;
+
+// The plan counts the SMs of the one part this library is built for, so that a workspace
+// can be sized without a device.
+constexpr int kSms = 148;
+constexpr int64_t kPieceBlocks = 8;  // 512 of k per piece of a Sum variant
+constexpr int64_t kFlipTokens = 64;  // most tokens the flipped tiles take
 
 bool sizes_ok(int64_t rows, int64_t in, int64_t out) {
   return rows >= 0 && rows <= kMaxRows && in >= 1 && in <= kMaxSide && out >= 1 && out <= kMaxSide;
@@ -124,10 +107,274 @@ bool sizes_ok(int64_t rows, int64_t in, int64_t out) {
 
 bool act_ok(int act) { return act >= MUON_ACT_NONE && act <= MUON_ACT_SILU; }
 
-muon_status_t run_product(const ProductParams& p, cudaStream_t s) {
-  const dim3 g(static_cast<unsigned>(ceil_div(p.n, 64)), static_cast<unsigned>(ceil_div(p.m, 64)));
-  product_kernel<<<g, 256, 0, s>>>(p);
-  return launched();
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+EpiView epi_view(const muon_view_t& v, int64_t rows, int64_t cols) {
+  EpiView e{v.data, row_stride(v, rows, cols), v.dtype == MUON_BF16 ? 1 : 0, 0};
+  const size_t pitch = static_cast<size_t>(e.ld) * elem_bytes(v.dtype);
+  const bool one = rows <= 1;
+  for (int k = 1; k <= 2; ++k)
+    if (aligned_bytes(v.data, 16 * k) && (one || pitch % (16 * k) == 0)) e.vec = k;
+  return e;
+}
+
+// An operand of a product: a stored matrix as the tensor cores will read it.
+struct Operand {
+  const muon_view_t* v = nullptr;
+  int64_t rows = 0, cols = 0;
+  int terms = 1;
+  bool direct = true;     // read in place
+  size_t offset = 0;      // of the packed terms in the workspace
+  int64_t ld_packed = 0;  // elements, a multiple of 8
+
+  Operand() = default;
+  Operand(const muon_view_t& view, int64_t r, int64_t c) : v(&view), rows(r), cols(c) {
+    terms = view.dtype == MUON_F32 ? kTerms : 1;
+    const int64_t ld = row_stride(view, r, c);
+    direct = terms == 1 && aligned_bytes(view.data, 16) && (r <= 1 || ld % 8 == 0);
+    ld_packed = ceil_div(c, 8) * 8;
+  }
+  size_t term_bytes() const { return up(static_cast<size_t>(rows) * ld_packed * 2); }
+  size_t bytes() const { return direct ? 0 : terms * term_bytes(); }
+  void place(size_t* at) {
+    offset = *at;
+    *at += bytes();
+  }
+};
+
+// How a product runs.  m, n: the output's rows and columns; k: the reduction.
+struct Plan {
+  int tile = kOne128;
+  int64_t tiles_m = 0, tiles_n = 0, nk = 0, splits = 1, kb_per_split = 0;
+  int nseg = 1;
+  bool join = false;  // through partial sums and the join kernel
+  size_t partial_bytes = 0;
+  int64_t ld_partial = 0;
+};
+
+int segments(int ta, int tb) { return ta == 1 ? tb : (tb == 1 ? ta : kMaxSegments); }
+
+// Picks the tile and the number of splits with the least estimated time, in SM cycles:
+// waves of units times their k-blocks, and for a join the partial sums' way out and back.
+// sum: some output is fp32.  raw: the epilogue does no more than add and store fp32.
+Plan make_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, bool may_flip) {
+  Plan best;
+  double least = 1e30;
+  const int64_t nk = ceil_div(k, kProductBK);
+  for (int tile = kPair256; tile <= kFlip64; ++tile) {
+    if (tile == (sum ? kPair256 : kPair256Sum)) continue;
+    const bool flip = tile >= kFlip32;
+    if (flip && (!may_flip || m > product_tile_n(tile))) continue;
+    if (!flip && may_flip && m <= kFlipTokens) continue;
+    const int64_t tm = ceil_div(flip ? n : m, product_tile_m(tile)), tn = ceil_div(flip ? m : n, product_tile_n(tile));
+    const int64_t workers = tile <= kPair256Sum ? kSms / 2 : kSms;
+    const double block = (tile <= kPair256Sum ? 512.0 : tile == kOne128 ? 450.0 : 320.0) * nseg;
+    if (tm * tn > 0x3fffffff) continue;
+    for (int64_t want = 1; want <= 32; ++want) {
+      const int64_t per = ceil_div(nk, want), splits = ceil_div(nk, per);
+      if (splits != want || (want > 1 && per < 2) || tm * tn * splits > 0x3fffffff) continue;
+      const double waves = static_cast<double>(ceil_div(tm * tn * splits, workers));
+      double cost = waves * (per * block + 600.0) + 3000.0;
+      const bool join = splits > 1 || (tile == kPair256Sum && !raw);
+      if (join) cost += 3500.0 + static_cast<double>(splits + 1) * m * n * 4.0 / 3000.0;
+      if (cost < least) {
+        least = cost;
+        best.tile = tile;
+        best.tiles_m = tm;
+        best.tiles_n = tn;
+        best.splits = splits;
+        best.kb_per_split = per;
+        best.join = join;
+      }
+    }
+  }
+  best.nk = nk;
+  best.nseg = nseg;
+  if (best.join) {
+    best.ld_partial = ceil_div(n, 32) * 32;
+    best.partial_bytes = up(static_cast<size_t>(best.splits) * m * best.ld_partial * 4);
+  }
+  return best;
+}
+
+muon_status_t pack(const Operand& o, uint8_t* ws, cudaStream_t s) {
+  if (o.direct || o.rows == 0) return MUON_OK;
+  const EpiView src = epi_view(*o.v, o.rows, o.cols);
+  PackParams p{};
+  p.src = src.p;
+  p.dst = reinterpret_cast<__nv_bfloat16*>(ws + o.offset);
+  p.rows = o.rows;
+  p.ld_src = src.ld;
+  p.ld_dst = o.ld_packed;
+  p.term_stride = static_cast<int64_t>(o.term_bytes() / 2);
+  p.cols = static_cast<int32_t>(o.cols);
+  p.src_bf16 = src.bf16;
+  p.terms = o.terms;
+  p.vec = src.vec;
+  return launch_pack(p, kSms, s) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+// `side_rows`: how many of the operand's side a box of a K-major operand covers.
+bool operand_maps(CUtensorMap* maps, const Operand& o, uint8_t* ws, bool mn, int side_rows) {
+  for (int t = 0; t < o.terms; ++t) {
+    const void* base = o.direct ? o.v->data : ws + o.offset + t * o.term_bytes();
+    const int64_t ld = o.direct ? (o.rows <= 1 ? ceil_div(o.cols, 8) * 8 : o.v->ld) : o.ld_packed;
+    if (!encode_operand_map(&maps[t], base, o.rows, o.cols, ld, mn ? 64 : side_rows)) return false;
+  }
+  return true;
+}
+
+// a: the operand on the output's row side; b: on its column side.  mn: contiguous along the side.
+muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const Epilogue& e,
+                          uint8_t* ws, size_t partial_at, cudaStream_t s) {
+  static const uint8_t both_a[kMaxSegments] = {0, 2, 1, 0, 1, 0}, both_b[kMaxSegments] = {2, 0, 1, 1, 0, 0};
+  const bool flip = pl.tile >= kFlip32;
+  const Operand &am = flip ? b : a, &bm = flip ? a : b;
+  ProductParams p{};
+  p.a_mn = flip ? b_mn : a_mn;
+  p.b_mn = flip ? a_mn : b_mn;
+  if (!operand_maps(p.map_a, am, ws, p.a_mn, 128) ||
+      !operand_maps(p.map_b, bm, ws, p.b_mn, pl.tile <= kPair256Sum ? 128 : product_tile_n(pl.tile)))
+    return MUON_ERR_CUDA;
+  p.e = e;
+  p.tiles_m = static_cast<int32_t>(pl.tiles_m);
+  p.tiles_n = static_cast<int32_t>(pl.tiles_n);
+  p.nk = static_cast<int32_t>(pl.nk);
+  p.splits = static_cast<int32_t>(pl.splits);
+  p.kb_per_split = static_cast<int32_t>(pl.kb_per_split);
+  p.piece = pl.tile == kPair256 ? p.kb_per_split : static_cast<int32_t>(kPieceBlocks);
+  p.nseg = pl.nseg;
+  for (int g = 0; g < pl.nseg; ++g) {  // the smallest products first
+    p.seg_a[g] = static_cast<uint8_t>(am.terms == 1 ? 0 : bm.terms == 1 ? pl.nseg - 1 - g : both_a[g]);
+    p.seg_b[g] = static_cast<uint8_t>(bm.terms == 1 ? 0 : am.terms == 1 ? pl.nseg - 1 - g : both_b[g]);
+  }
+  p.timeout_ns = layers_wait_ns();
+  if (pl.join) {
+    p.partial = reinterpret_cast<float*>(ws + partial_at);
+    p.ld_partial = pl.ld_partial;
+    p.split_stride = e.rows * pl.ld_partial;
+  }
+  if (launch_product(pl.tile, p, kSms, s) != cudaSuccess) return MUON_ERR_CUDA;
+  if (pl.join) {
+    JoinParams j{};
+    j.e = e;
+    j.partial = p.partial;
+    j.ld_partial = p.ld_partial;
+    j.split_stride = p.split_stride;
+    j.splits = p.splits;
+    if (launch_join(j, kSms, s) != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  return MUON_OK;
+}
+
+bool wants_sum(const muon_view_t& out) { return out.data != nullptr && out.dtype == MUON_F32; }
+
+struct LinearPlan {
+  Operand x, w;
+  Plan z;
+  size_t partial_at = 0, bytes = 0;
+};
+
+LinearPlan plan_linear(const muon_linear_t* d) {
+  LinearPlan pl;
+  if (d->rows == 0) return pl;
+  pl.x = Operand(d->x, d->rows, d->in);
+  pl.w = Operand(d->w, d->out, d->in);
+  pl.z = make_plan(d->rows, d->out, d->in, segments(pl.x.terms, pl.w.terms), wants_sum(d->y) || wants_sum(d->preact),
+                   false, true);
+  pl.x.place(&pl.bytes);
+  pl.w.place(&pl.bytes);
+  pl.partial_at = pl.bytes;
+  pl.bytes += pl.z.partial_bytes;
+  return pl;
+}
+
+struct LinearGradPlan {
+  Operand dy, x, w;
+  Plan dx, dw;
+  int64_t slices = 0;
+  size_t partial_at = 0, db_at = 0, bytes = 0;
+};
+
+LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
+  LinearGradPlan pl;
+  if (d->rows == 0) return pl;
+  const bool dx = d->dx.data != nullptr, dw = d->dw.data != nullptr;
+  pl.dy = Operand(d->dy, d->rows, d->out);
+  if (dx || dw) pl.dy.place(&pl.bytes);
+  size_t partial = 0;
+  if (dx) {
+    pl.w = Operand(d->w, d->out, d->in);
+    pl.w.place(&pl.bytes);
+    pl.dx = make_plan(d->rows, d->in, d->out, segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), false, true);
+    partial = pl.dx.partial_bytes;
+  }
+  if (dw) {
+    pl.x = Operand(d->x, d->rows, d->in);
+    pl.x.place(&pl.bytes);
+    pl.dw = make_plan(d->out, d->in, d->rows, segments(pl.dy.terms, pl.x.terms), true, true, false);
+    partial = std::max(partial, pl.dw.partial_bytes);  // the products run one after the other
+  }
+  pl.partial_at = pl.bytes;
+  pl.bytes += partial;
+  if (d->db != nullptr) {
+    pl.slices = std::max<int64_t>(1, std::min(ceil_div(d->rows, 64), 4 * kSms / ceil_div(d->out, 256)));
+    pl.db_at = pl.bytes;
+    pl.bytes += up(static_cast<size_t>(pl.slices) * d->out * 4);
+  }
+  return pl;
+}
+
+muon_status_t take_workspace(Operands* ops, void* ws, size_t have, size_t need) {
+  if (ops->status != MUON_OK || need == 0) return ops->status;
+  if (ws == nullptr || have < need) return MUON_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned_bytes(ws, 256)) return MUON_ERR_ALIGNMENT;
+  ops->add_bytes(ws, need);
+  return MUON_OK;
+}
+
+template <class K, class P>
+muon_status_t launch_after(K kernel, const P& p, dim3 grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+// The checks of a descriptor without its workspace, so that sizing a call checks it too.
+muon_status_t check_linear(const muon_linear_t* d, Operands* ops) {
+  if (d == nullptr || !act_ok(d->act)) return MUON_ERR_INVALID_ARG;
+  if (!sizes_ok(d->rows, d->in, d->out)) return MUON_ERR_UNSUPPORTED_SHAPE;
+  ops->add(d->x, d->rows, d->in, true, false);
+  ops->add(d->w, d->out, d->in, true, false);
+  ops->add(d->bias, 1, d->out, false, false);
+  if (!same_view(d->y, d->residual, d->rows)) ops->add(d->residual, d->rows, d->out, false, false);
+  ops->add(d->y, d->rows, d->out, true, true);
+  ops->add(d->preact, d->rows, d->out, false, true);
+  return ops->status;
+}
+
+muon_status_t check_linear_grad(const muon_linear_grad_t* d, Operands* ops) {
+  if (d == nullptr || !act_ok(d->in_act) || (d->accumulate != 0 && d->accumulate != 1)) return MUON_ERR_INVALID_ARG;
+  if (!sizes_ok(d->rows, d->in, d->out)) return MUON_ERR_UNSUPPORTED_SHAPE;
+  const bool dx = d->dx.data != nullptr, dw = d->dw.data != nullptr, slope = dx && d->in_act != MUON_ACT_NONE;
+  ops->add(d->dy, d->rows, d->out, true, false);
+  ops->add(d->x, d->rows, d->in, dw, false);
+  ops->add(d->w, d->out, d->in, dx, false);
+  ops->add(d->preact, d->rows, d->in, slope, false);
+  if (!(dx && same_view(d->dx, d->skip, d->rows))) ops->add(d->skip, d->rows, d->in, false, false);
+  ops->add(d->dx, d->rows, d->in, false, true);
+  ops->add(d->dw, d->out, d->in, false, true);
+  ops->add_f32(d->db, d->out, false, true);
+  if (dw && d->dw.dtype != MUON_F32) ops->fail(MUON_ERR_UNSUPPORTED_DTYPE);
+  if (!dx && !dw && d->db == nullptr && d->rows > 0) ops->fail(MUON_ERR_INVALID_ARG);
+  return ops->status;
 }
 
 }  // namespace
@@ -135,141 +382,110 @@ muon_status_t run_product(const ProductParams& p, cudaStream_t s) {
 extern "C" {
 
 muon_status_t muon_linear_workspace(const muon_linear_t* d, size_t* bytes) {
-  if (d == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
-  if (!sizes_ok(d->rows, d->in, d->out)) return MUON_ERR_UNSUPPORTED_SHAPE;
-  *bytes = 0;
+  Operands ops;
+  const muon_status_t st = check_linear(d, &ops);
+  if (st != MUON_OK) return st;
+  if (bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  *bytes = plan_linear(d).bytes;
   return MUON_OK;
 }
 
 muon_status_t muon_linear(const muon_linear_t* d, void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
-  if (d == nullptr || !act_ok(d->act)) return MUON_ERR_INVALID_ARG;
-  if (!sizes_ok(d->rows, d->in, d->out)) return MUON_ERR_UNSUPPORTED_SHAPE;
   Operands ops;
-  ops.add(d->x, d->rows, d->in, true, false);
-  ops.add(d->w, d->out, d->in, true, false);
-  ops.add(d->bias, 1, d->out, false, false);
-  if (!same_view(d->y, d->residual, d->rows)) ops.add(d->residual, d->rows, d->out, false, false);
-  ops.add(d->y, d->rows, d->out, true, true);
-  ops.add(d->preact, d->rows, d->out, false, true);
-  muon_status_t st = ops.check();
+  muon_status_t st = check_linear(d, &ops);
   if (st != MUON_OK) return st;
+  const LinearPlan pl = plan_linear(d);
+  if ((st = take_workspace(&ops, workspace, workspace_bytes, pl.bytes)) != MUON_OK) return st;
+  if ((st = ops.check()) != MUON_OK) return st;
   int sms = 0;
   if ((st = layers_device(&sms)) != MUON_OK) return st;
   if (d->rows == 0) return MUON_OK;
-  ProductParams p{};
-  p.a = d->x.data;
-  p.a_side = row_stride(d->x, d->rows, d->in);
-  p.a_k = 1;
-  p.a_bf16 = d->x.dtype == MUON_BF16;
-  p.b = d->w.data;
-  p.b_side = row_stride(d->w, d->out, d->in);
-  p.b_k = 1;
-  p.b_bf16 = d->w.dtype == MUON_BF16;
-  p.m = d->rows;
-  p.n = d->out;
-  p.k = d->in;
-  p.bias = d->bias.data;
-  p.bias_bf16 = d->bias.dtype == MUON_BF16;
-  p.preact = d->preact.data;
-  p.ld_preact = row_stride(d->preact, d->rows, d->out);
-  p.preact_bf16 = d->preact.dtype == MUON_BF16;
-  p.act = d->act;
-  p.add = d->residual.data;
-  p.ld_add = row_stride(d->residual, d->rows, d->out);
-  p.add_bf16 = d->residual.dtype == MUON_BF16;
-  p.out = d->y.data;
-  p.ld_out = row_stride(d->y, d->rows, d->out);
-  p.out_bf16 = d->y.dtype == MUON_BF16;
-  return run_product(p, static_cast<cudaStream_t>(stream));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = pack(pl.x, ws, s)) != MUON_OK || (st = pack(pl.w, ws, s)) != MUON_OK) return st;
+  Epilogue e{};
+  e.rows = d->rows;
+  e.cols = d->out;
+  e.bias = epi_view(d->bias, 1, d->out);
+  e.preact = epi_view(d->preact, d->rows, d->out);
+  e.add = epi_view(d->residual, d->rows, d->out);
+  e.out = epi_view(d->y, d->rows, d->out);
+  e.act = d->act;
+  return run_product(pl.z, pl.x, false, pl.w, false, e, ws, pl.partial_at, s);
 }
 
 muon_status_t muon_linear_backward_workspace(const muon_linear_grad_t* d, size_t* bytes) {
-  if (d == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
-  if (!sizes_ok(d->rows, d->in, d->out)) return MUON_ERR_UNSUPPORTED_SHAPE;
-  *bytes = 0;
+  Operands ops;
+  const muon_status_t st = check_linear_grad(d, &ops);
+  if (st != MUON_OK) return st;
+  if (bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  *bytes = plan_linear_grad(d).bytes;
   return MUON_OK;
 }
 
 muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace, size_t workspace_bytes,
                                    void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
-  if (d == nullptr || !act_ok(d->in_act) || (d->accumulate != 0 && d->accumulate != 1)) return MUON_ERR_INVALID_ARG;
-  if (!sizes_ok(d->rows, d->in, d->out)) return MUON_ERR_UNSUPPORTED_SHAPE;
-  const bool dx = d->dx.data != nullptr, dw = d->dw.data != nullptr, slope = dx && d->in_act != MUON_ACT_NONE;
   Operands ops;
-  ops.add(d->dy, d->rows, d->out, true, false);
-  ops.add(d->x, d->rows, d->in, dw, false);
-  ops.add(d->w, d->out, d->in, dx, false);
-  ops.add(d->preact, d->rows, d->in, slope, false);
-  if (!(dx && same_view(d->dx, d->skip, d->rows))) ops.add(d->skip, d->rows, d->in, false, false);
-  ops.add(d->dx, d->rows, d->in, false, true);
-  ops.add(d->dw, d->out, d->in, false, true);
-  ops.add_f32(d->db, d->out, false, true);
-  if (dw && d->dw.dtype != MUON_F32) ops.fail(MUON_ERR_UNSUPPORTED_DTYPE);
-  if (!dx && !dw && d->db == nullptr && d->rows > 0) ops.fail(MUON_ERR_INVALID_ARG);
-  muon_status_t st = ops.check();
+  muon_status_t st = check_linear_grad(d, &ops);
   if (st != MUON_OK) return st;
+  const LinearGradPlan pl = plan_linear_grad(d);
+  if ((st = take_workspace(&ops, workspace, workspace_bytes, pl.bytes)) != MUON_OK) return st;
+  if ((st = ops.check()) != MUON_OK) return st;
   int sms = 0;
   if ((st = layers_device(&sms)) != MUON_OK) return st;
+  const bool dx = d->dx.data != nullptr, dw = d->dw.data != nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dx && d->rows > 0) {
-    ProductParams p{};
-    p.a = d->dy.data;
-    p.a_side = row_stride(d->dy, d->rows, d->out);
-    p.a_k = 1;
-    p.a_bf16 = d->dy.dtype == MUON_BF16;
-    p.b = d->w.data;
-    p.b_side = 1;
-    p.b_k = row_stride(d->w, d->out, d->in);
-    p.b_bf16 = d->w.dtype == MUON_BF16;
-    p.m = d->rows;
-    p.n = d->in;
-    p.k = d->out;
-    p.slope = slope ? d->preact.data : nullptr;
-    p.ld_slope = row_stride(d->preact, d->rows, d->in);
-    p.slope_bf16 = d->preact.dtype == MUON_BF16;
-    p.slope_act = d->in_act;
-    p.add = d->skip.data;
-    p.ld_add = row_stride(d->skip, d->rows, d->in);
-    p.add_bf16 = d->skip.dtype == MUON_BF16;
-    p.out = d->dx.data;
-    p.ld_out = row_stride(d->dx, d->rows, d->in);
-    p.out_bf16 = d->dx.dtype == MUON_BF16;
-    if ((st = run_product(p, s)) != MUON_OK) return st;
+  if (d->rows == 0) {  // the sums are empty
+    if (d->accumulate) return MUON_OK;
+    const size_t pitch = static_cast<size_t>(row_stride(d->dw, d->out, d->in)) * 4;
+    if (dw && cudaMemset2DAsync(d->dw.data, pitch, 0, static_cast<size_t>(d->in) * 4, d->out, s) != cudaSuccess)
+      return MUON_ERR_CUDA;
+    if (d->db != nullptr && cudaMemsetAsync(d->db, 0, static_cast<size_t>(d->out) * 4, s) != cudaSuccess)
+      return MUON_ERR_CUDA;
+    return MUON_OK;
   }
-  if (dw && !(d->rows == 0 && d->accumulate)) {
-    ProductParams p{};
-    p.a = d->dy.data;
-    p.a_side = 1;
-    p.a_k = row_stride(d->dy, d->rows, d->out);
-    p.a_bf16 = d->dy.dtype == MUON_BF16;
-    p.b = d->x.data;
-    p.b_side = 1;
-    p.b_k = row_stride(d->x, d->rows, d->in);
-    p.b_bf16 = d->x.dtype == MUON_BF16;
-    p.m = d->out;
-    p.n = d->in;
-    p.k = d->rows;
-    p.out = d->dw.data;
-    p.ld_out = row_stride(d->dw, d->out, d->in);
-    p.add = d->accumulate ? d->dw.data : nullptr;
-    p.ld_add = p.ld_out;
-    if ((st = run_product(p, s)) != MUON_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (dx || dw)
+    if ((st = pack(pl.dy, ws, s)) != MUON_OK) return st;
+  if (dx) {
+    if ((st = pack(pl.w, ws, s)) != MUON_OK) return st;
+    Epilogue e{};
+    e.rows = d->rows;
+    e.cols = d->in;
+    if (d->in_act != MUON_ACT_NONE) {
+      e.slope = epi_view(d->preact, d->rows, d->in);
+      e.slope_act = d->in_act;
+    }
+    e.add = epi_view(d->skip, d->rows, d->in);
+    e.out = epi_view(d->dx, d->rows, d->in);
+    if ((st = run_product(pl.dx, pl.dy, false, pl.w, true, e, ws, pl.partial_at, s)) != MUON_OK) return st;
   }
-  if (d->db != nullptr && !(d->rows == 0 && d->accumulate)) {
+  if (dw) {
+    if ((st = pack(pl.x, ws, s)) != MUON_OK) return st;
+    Epilogue e{};
+    e.rows = d->out;
+    e.cols = d->in;
+    e.out = epi_view(d->dw, d->out, d->in);
+    if (d->accumulate) e.add = e.out;
+    if ((st = run_product(pl.dw, pl.dy, true, pl.x, true, e, ws, pl.partial_at, s)) != MUON_OK) return st;
+  }
+  if (d->db != nullptr) {
+    const EpiView dy = epi_view(d->dy, d->rows, d->out);
     ColumnSumParams c{};
-    c.dy = d->dy.data;
+    c.dy = dy.p;
     c.db = d->db;
+    c.partial = reinterpret_cast<float*>(ws + pl.db_at);
     c.rows = d->rows;
-    c.ld = row_stride(d->dy, d->rows, d->out);
+    c.ld = dy.ld;
+    c.ld_partial = d->out;
     c.cols = static_cast<int32_t>(d->out);
-    c.bf16 = d->dy.dtype == MUON_BF16;
+    c.bf16 = dy.bf16;
+    c.vec = dy.vec;
     c.accumulate = d->accumulate;
-    column_sum_kernel<<<static_cast<unsigned>(ceil_div(d->out, 32)), 256, 0, s>>>(c);
-    return launched();
+    c.slices = static_cast<int32_t>(pl.slices);
+    const unsigned blocks = static_cast<unsigned>(ceil_div(d->out, 256));
+    if ((st = launch_after(muon_column_sum_kernel, c, dim3(blocks, c.slices), s)) != MUON_OK) return st;
+    return launch_after(muon_column_join_kernel, c, dim3(blocks), s);
   }
   return MUON_OK;
 }
@@ -288,37 +504,15 @@ muon_status_t muon_activation_backward(const muon_activation_grad_t* d, void* st
   if ((st = layers_device(&sms)) != MUON_OK) return st;
   if (d->rows == 0) return MUON_OK;
   ActGradParams p{};
-  p.dy = d->dy.data;
-  p.z = d->z.data;
-  p.dz = d->dz.data;
+  p.dy = epi_view(d->dy, d->rows, d->cols);
+  p.z = epi_view(d->z, d->rows, d->cols);
+  p.dz = epi_view(d->dz, d->rows, d->cols);
   p.rows = d->rows;
   p.cols = d->cols;
-  p.ld_dy = row_stride(d->dy, d->rows, d->cols);
-  p.ld_z = row_stride(d->z, d->rows, d->cols);
-  p.ld_dz = row_stride(d->dz, d->rows, d->cols);
-  p.dy_bf16 = d->dy.dtype == MUON_BF16;
-  p.z_bf16 = d->z.dtype == MUON_BF16;
   p.act = d->act;
-  const int64_t blocks = std::min<int64_t>(d->rows * ceil_div(d->cols, 256), sms * 64);
-  activation_backward_kernel<<<static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return launched();
-}
-
-muon_status_t muon_layers_status(void* stream, int clear, int32_t* device_status, int32_t* where) {
-  if (device_status == nullptr) return MUON_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int32_t h[2] = {0, 0};
-  const int32_t zero[2] = {0, 0};
-  if (cudaMemcpyFromSymbolAsync(h, g_layers_status, sizeof(h), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return MUON_ERR_CUDA;
-  if (clear && (cudaMemcpyToSymbolAsync(g_layers_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) !=
-                    cudaSuccess ||
-                cudaStreamSynchronize(s) != cudaSuccess))
-    return MUON_ERR_CUDA;
-  *device_status = h[0];
-  if (where != nullptr) *where = h[1];
-  return MUON_OK;
+  const int64_t blocks = std::min<int64_t>(ceil_div(d->rows * ceil_div(d->cols, 8), 256), int64_t(kSms) * 32);
+  return launch_after(muon_activation_backward_kernel, p, dim3(static_cast<unsigned>(blocks)),
+                      static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

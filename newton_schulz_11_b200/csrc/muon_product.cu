@@ -1,0 +1,636 @@
+// The products of the layers on the 5th-generation tensor cores (tcgen05, sm_100a).
+//
+//   D[M x N] = sum_k A(m, k) B(n, k), then the epilogue of muon_epilogue.cuh
+//
+// One persistent, warp-specialised kernel serves x W^T (both operands contiguous along k),
+// dy W (W contiguous along its side) and dy^T x (both contiguous along their sides): the
+// majorness of each operand is a run-time property of the launch.
+//
+// Operand precision.  A bf16 operand is read as it is.  An fp32 operand comes as three bf16
+// terms, x = h + m + l exactly (muon_linear.cu), and the product as the sum of the term
+// products whose size is at least 2^-16 of the whole: h h, h m, m h, m m, h l, l h (six),
+// or h b, m b, l b against a bf16 operand (three).  The k-blocks of a piece are walked once
+// per term product, the smallest first, all into one accumulator.
+//
+// Sums.  The tensor cores add 16 products at a time to the fp32 accumulator and truncate.
+// Left alone that costs about 1.1e-9 K relative for zero-mean data (measured: 9e-6 at
+// K = 8192, 1.9e-5 at K = 16384), far below a bf16 output's half step but not below fp32's.  The
+// Sum variants therefore end the accumulation after 512 of k, read the accumulator into
+// registers and add it there with rounding to nearest (measured: see below).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "muon_epilogue.cuh"
+#include "muon_layers_host.h"
+
+namespace muon {
+
+__device__ int32_t g_layers_status[2];  // code, wait site
+
+enum ProductSite : int {
+  kSiteLoad = 1,      // producer: a stage to be consumed
+  kSiteAccFree = 2,   // MMA issuer: an accumulator to be read
+  kSiteStage = 3,     // MMA issuer: a stage to be filled
+  kSiteAccReady = 4,  // epilogue: an accumulator to be finished
+};
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The box lands in this CTA; its bytes complete on the leader CTA's mbarrier.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t c0,
+                                                 int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar_cluster)
+      : "memory");
+}
+
+template <int NC>
+__device__ __forceinline__ void tmem_load_row(uint32_t taddr, uint32_t (&v)[NC]) {
+  if constexpr (NC == 32)
+    tmem_ld_32x32b_x32(taddr, v);
+  else
+    tmem_ld_32x32b_x16(taddr, v);
+  tmem_wait_ld();
+}
+
+// Per-CTA layout of a variant.  CG CTAs share a tile of 128 CG x TN; each stages its own 128
+// rows of A and TN / CG rows of B, 64 deep.
+// SUM: the reduction in pieces added in registers.  FLIP: the tile's rows are the output's
+// columns.  RAW: the epilogue only adds and stores fp32 (a pair's 128 sums a thread leave no
+// registers for more; what needs more goes through partial sums and the join kernel).
+template <int CG_, int TN_, bool SUM_, bool FLIP_, bool RAW_>
+struct Product {
+  static constexpr int CG = CG_, TM = 128 * CG_, TN = TN_, TNB = TN_ / CG_;
+  static constexpr bool SUM = SUM_, FLIP = FLIP_, RAW = RAW_;
+  static constexpr int BK = kProductBK;
+  static constexpr int kABytes = 128 * BK * 2;
+  static constexpr int kBBytes = TNB * BK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int S = (232448 - 1024 - 256) / kStageBytes < 10 ? (232448 - 1024 - 256) / kStageBytes : 10;
+  static constexpr int kBarOff = S * kStageBytes;
+  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+  static constexpr int NEPI = 8;              // epilogue warps
+  static constexpr int kThreads = 64 + 32 * NEPI;
+  static constexpr int NCW = TN / 2;          // accumulator columns per epilogue thread
+  static constexpr int NC = SUM ? 16 : 32;                // read from tensor memory at a time
+  static constexpr int FC = FLIP ? 16 : SUM ? 8 : 32;     // finished at a time
+  static constexpr int kTmemCols = 2 * TN;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
+  static_assert((2 * S + 5) * 8 + 16 <= 256, "barrier area");
+};
+
+// One unit of work: a tile and a range of k-blocks.
+struct Unit {
+  int i, j, split, kb0, kb1;
+};
+
+// Tiles are walked in bands of 8 along M, so that the tiles in flight at one time share
+// rows of A and of B in L2.
+__device__ __forceinline__ Unit decode_unit(const ProductParams& p, int t) {
+  const int tiles = p.tiles_m * p.tiles_n;
+  Unit u;
+  u.split = t / tiles;
+  const int q = t - u.split * tiles;
+  const int band = q / (8 * p.tiles_n);
+  const int first = 8 * band;
+  const int height = p.tiles_m - first < 8 ? p.tiles_m - first : 8;
+  const int in = q - band * 8 * p.tiles_n;
+  u.j = in / height;
+  u.i = first + (in - u.j * height);
+  u.kb0 = u.split * p.kb_per_split;
+  u.kb1 = u.kb0 + p.kb_per_split < p.nk ? u.kb0 + p.kb_per_split : p.nk;
+  return u;
+}
+
+// One operand's k-block into `dst`: ROWS of its side from side0, 64 of k from k0.
+// K-major: one box of 64 k x ROWS.  Side-major (ROWS = 128): two boxes of 64 x 64 k.
+template <int CG, int ROWS>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int mn, int side0, int k0,
+                                             uint64_t* bar, uint32_t bar_cluster) {
+  if (mn) {
+#pragma unroll
+    for (int b = 0; b < ROWS / 64; ++b) {
+      if constexpr (CG == 2)
+        tma_load_2d_pair(dst + b * 8192, map, bar_cluster, side0 + 64 * b, k0);
+      else
+        tma_load_2d(dst + b * 8192, map, bar, side0 + 64 * b, k0);
+    }
+  } else {
+    if constexpr (CG == 2)
+      tma_load_2d_pair(dst, map, bar_cluster, k0, side0);
+    else
+      tma_load_2d(dst, map, bar, k0, side0);
+  }
+}
+
+// Descriptor of the kk-th 16 of k: K-major rows of 128 B, 32 B per slice; side-major k-rows of
+// 128 B, 2 KB per slice, the next 64 of the side 8 KB on.
+__device__ __forceinline__ uint64_t slice_desc(uint32_t addr, int mn, int kk) {
+  return mn ? smem_desc_sw128(addr + kk * 2048u, 8192u, 1024u) : smem_desc_sw128(addr + kk * 32u, 16u, 1024u);
+}
+
+__device__ __forceinline__ void settle_wait(uint64_t* bar, uint32_t parity, unsigned long long budget) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < budget) {
+  }
+}
+
+// Lane 0 waits, the warp learns the outcome.
+__device__ __forceinline__ bool warp_waits(uint64_t* bar, uint32_t parity, const Watchdog& w, int site) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, w, site) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+template <class L>
+__global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __grid_constant__ ProductParams p) {
+  constexpr int CG = L::CG, S = L::S, TN = L::TN, NC = L::NC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // used in the leader CTA
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + 2;  // used in the leader CTA: every epilogue warp of the pair arrives
+  uint64_t* tdown = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdown + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* peer_issued = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);  // leader CTA
+  __shared__ uint64_t pdone;  // leader CTA: the peer's producer has finished
+
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
+  const int worker = CG == 2 ? blockIdx.x >> 1 : blockIdx.x;
+  const int workers = CG == 2 ? gridDim.x >> 1 : gridDim.x;
+  const int units = p.tiles_m * p.tiles_n * p.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], CG * L::NEPI);
+    }
+    mbar_init(tdown, 1);
+    mbar_init(&pdone, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.map_a[0]);
+    tma_prefetch_desc(&p.map_b[0]);
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(tmem_slot, L::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, L::kTmemCols);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Watchdog wd{abort_flag, g_layers_status, p.timeout_ns};
+  // waits on the way out, for copies and MMAs in flight, end by themselves
+  const unsigned long long tb = p.timeout_ns > 2000000000ull ? p.timeout_ns : 2000000000ull;
+  griddep_wait();  // everything read or written below may belong to the launch before
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer (each CTA)
+    // Load i of a CTA goes to stage i % S in phase i / S; the leader arms each phase for the
+    // whole pair's bytes.
+    if (lane == 0) {
+      const uint32_t full0 = map_to_rank(smem_u32(full), 0);
+      int s = 0;
+      uint32_t ph = 0, issued = 0;
+      bool ok = true;
+      for (int t = worker; ok && t < units; t += workers) {
+        const Unit u = decode_unit(p, t);
+        const int a0 = L::TM * u.i + 128 * rank;
+        const int b0 = TN * u.j + L::TNB * rank;
+        for (int pb = u.kb0; ok && pb < u.kb1; pb += p.piece) {
+          const int pe = pb + p.piece < u.kb1 ? pb + p.piece : u.kb1;
+          for (int g = 0; ok && g < p.nseg; ++g) {
+            const CUtensorMap* ma = &p.map_a[p.seg_a[g]];
+            const CUtensorMap* mb = &p.map_b[p.seg_b[g]];
+            for (int kb = pb; kb < pe; ++kb) {
+              if (!mbar_wait(&empty[s], ph ^ 1u, wd, kSiteLoad)) {
+                ok = false;
+                break;
+              }
+              uint8_t* sa = smem + s * L::kStageBytes;
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * L::kStageBytes);
+              const uint32_t fb = full0 + 8u * static_cast<uint32_t>(s);
+              load_operand<CG, 128>(sa, ma, p.a_mn, a0, kb * L::BK, &full[s], fb);
+              load_operand<CG, L::TNB>(sa + L::kABytes, mb, p.b_mn, b0, kb * L::BK, &full[s], fb);
+              ++issued;
+              if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+              }
+            }
+          }
+        }
+      }
+      // Before the CTAs part, every copy in flight has landed.  A load below
+      // min(own, peer's) - S has: both producers waited for its stage to be consumed again.
+      // After a timeout the two may have stopped at different counts: the peer reports its
+      // own, and the leader completes or arms the difference, phase by phase in order.
+      if (rank != 0) {
+        st_cluster_u32(map_to_rank(smem_u32(const_cast<uint32_t*>(peer_issued)), 0), issued);
+        mbar_arrive_cluster(map_to_rank(smem_u32(&pdone), 0));
+      } else {
+        const uint32_t own = issued;
+        uint32_t peer = own;
+        if constexpr (CG == 2) {
+          const uint64_t t0 = global_timer_ns();
+          bool known;
+          while (!(known = mbar_try_wait_cluster(&pdone, 0)) && global_timer_ns() - t0 < tb) {
+          }
+          if (known) peer = *peer_issued;
+        }
+        const uint32_t both = own < peer ? own : peer, most = own > peer ? own : peer;
+        for (uint32_t i = both >= static_cast<uint32_t>(S) ? both - S : 0u; i < most; ++i) {
+          uint64_t* bar = &full[i % S];
+          if (i >= own)
+            mbar_arrive_expect_tx(bar, L::kStageBytes);
+          else if (i >= peer)
+            mbar_complete_tx(bar, L::kStageBytes);
+          settle_wait(bar, (i / S) & 1u, tb);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (leader CTA)
+    if (lane == 0) {
+      if (rank == 0) {
+        const uint32_t idesc = idesc_bf16_f32(L::TM, TN, p.a_mn, p.b_mn);
+        int s = 0, acc = 0;
+        uint32_t ph = 0, aph = 0;
+        bool ok = true;
+        for (int t = worker; ok && t < units; t += workers) {
+          const Unit u = decode_unit(p, t);
+          for (int pb = u.kb0; ok && pb < u.kb1; pb += p.piece) {
+            const int pe = pb + p.piece < u.kb1 ? pb + p.piece : u.kb1;
+            const int blocks = (pe - pb) * p.nseg;
+            if (!mbar_wait(&tempty[acc], aph ^ 1u, wd, kSiteAccFree)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t dtm = tmem_base + static_cast<uint32_t>(acc * TN);
+            for (int kb = 0; kb < blocks; ++kb) {
+              if (!mbar_wait(&full[s], ph, wd, kSiteStage)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sa = smem_u32(smem + s * L::kStageBytes);
+              const uint32_t sb = sa + L::kABytes;
+#pragma unroll
+              for (int kk = 0; kk < L::BK / 16; ++kk) {
+                if constexpr (CG == 2)
+                  umma_bf16_pair(dtm, slice_desc(sa, p.a_mn, kk), slice_desc(sb, p.b_mn, kk), idesc,
+                                 (kb | kk) != 0 ? 1u : 0u);
+                else
+                  umma_bf16(dtm, slice_desc(sa, p.a_mn, kk), slice_desc(sb, p.b_mn, kk), idesc,
+                            (kb | kk) != 0 ? 1u : 0u);
+              }
+              if constexpr (CG == 2)
+                umma_commit_pair(&empty[s], 0x3);
+              else
+                umma_commit(&empty[s]);
+              if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+              }
+            }
+            if (!ok) break;
+            if constexpr (CG == 2)
+              umma_commit_pair(&tfull[acc], 0x3);
+            else
+              umma_commit(&tfull[acc]);
+            if (++acc == 2) {
+              acc = 0;
+              aph ^= 1u;
+            }
+          }
+        }
+        // Every MMA has finished before either CTA releases tensor memory or leaves.
+        if constexpr (CG == 2)
+          umma_commit_pair(tdown, 0x3);
+        else
+          umma_commit(tdown);
+      }
+      settle_wait(tdown, 0, tb);
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue (each CTA)
+    const int ew = warp - 2;
+    const int q4 = warp & 3;  // tensor memory lanes 32 q4 .. 32 q4 + 31 belong to this warp
+    const int h = ew >> 2;    // which half of the tile's columns
+    const int r = q4 * 32 + lane;
+    const uint32_t tempty0 = map_to_rank(smem_u32(tempty), 0);
+    int acc = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int t = worker; ok && t < units; t += workers) {
+      const Unit u = decode_unit(p, t);
+      const int64_t row = static_cast<int64_t>(L::TM) * u.i + 128 * rank + r;
+      const int64_t col = static_cast<int64_t>(TN) * u.j + h * L::NCW;
+      float sum[L::SUM ? L::NCW : 1];
+#pragma unroll
+      for (int j = 0; j < (L::SUM ? L::NCW : 1); ++j) sum[j] = 0.f;
+      for (int pb = u.kb0; pb < u.kb1; pb += p.piece) {
+        ok = warp_waits(&tfull[acc], aph, wd, kSiteAccReady);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tacc = tmem_base + static_cast<uint32_t>(acc * TN + h * L::NCW) +
+                              (static_cast<uint32_t>(q4 * 32) << 16);
+        if constexpr (L::SUM) {
+#pragma unroll
+          for (int c = 0; c < L::NCW; c += NC) {
+            uint32_t v[NC];
+            tmem_load_row<NC>(tacc + c, v);
+#pragma unroll
+            for (int j = 0; j < NC; ++j) sum[c + j] += __uint_as_float(v[j]);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < L::NCW; c += NC) {
+            uint32_t v[NC];
+            tmem_load_row<NC>(tacc + c, v);
+            float x[NC];
+#pragma unroll
+            for (int j = 0; j < NC; ++j) x[j] = __uint_as_float(v[j]);
+            if (c + NC == L::NCW) {  // the last read: the accumulator is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8u * static_cast<uint32_t>(acc));
+            }
+            if (p.partial != nullptr) {
+              const EpiView out{p.partial + u.split * p.split_stride, p.ld_partial, 0, 2};
+              if (row < p.e.rows && col + c < p.ld_partial) store_segment<NC>(out, row * out.ld + col + c, NC, x);
+            } else {
+              finish_segment<NC>(p.e, row, col + c, x);
+            }
+          }
+        }
+        if constexpr (L::SUM) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8u * static_cast<uint32_t>(acc));
+        }
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1u;
+        }
+      }
+      if constexpr (L::SUM) {
+        if (!ok) break;
+        constexpr int FC = L::FC;
+        float* part = p.partial == nullptr ? nullptr : p.partial + u.split * p.split_stride;
+#pragma unroll
+        for (int c = 0; c < L::NCW; c += FC) {
+          float x[FC];
+#pragma unroll
+          for (int j = 0; j < FC; ++j) x[j] = sum[c + j];
+          if (part != nullptr) {
+            if constexpr (L::FLIP) {  // row: a feature; col: the first of FC tokens
+#pragma unroll
+              for (int j = 0; j < FC; ++j)
+                if (row < p.e.cols && col + c + j < p.e.rows) part[(col + c + j) * p.ld_partial + row] = x[j];
+            } else {
+              const EpiView out{part, p.ld_partial, 0, 2};
+              if (row < p.e.rows && col + c < p.ld_partial) store_segment<FC>(out, row * out.ld + col + c, FC, x);
+            }
+          } else if constexpr (L::RAW) {
+            const int64_t left = p.e.cols - col - c;
+            if (row < p.e.rows && left > 0) {
+              const int valid = left < FC ? static_cast<int>(left) : FC;
+              if (p.e.add.p != nullptr) {
+                float a[FC];
+                load_segment<FC>(p.e.add, row * p.e.add.ld + col + c, valid, a);
+#pragma unroll
+                for (int j = 0; j < FC; ++j) x[j] += a[j];
+              }
+              store_segment<FC>(p.e.out, row * p.e.out.ld + col + c, valid, x);
+            }
+          } else if constexpr (L::FLIP) {
+            finish_column<FC>(p.e, col + c, row, x);
+          } else {
+            finish_segment<FC>(p.e, row, col + c, x);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // nothing arrives on, or lands in, either CTA after this
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (CG == 2)
+      tmem_dealloc_pair(tmem_base, L::kTmemCols);
+    else
+      tmem_dealloc(tmem_base, L::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ joining split reductions
+
+// Adds the partial sums of a split reduction in the order of the splits, then the epilogue:
+// 8 columns of a row per thread.
+__global__ void __launch_bounds__(256) muon_join_kernel(const __grid_constant__ JoinParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t groups = (p.e.cols + 7) / 8;
+  const int64_t total = groups * p.e.rows;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t m = i / groups, n = (i - m * groups) * 8;
+    const float* src = p.partial + m * p.ld_partial + n;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    for (int s = 0; s < p.splits; ++s) {
+      const float4 a = *reinterpret_cast<const float4*>(src + s * p.split_stride);
+      const float4 b = *reinterpret_cast<const float4*>(src + s * p.split_stride + 4);
+      v[0] += a.x;
+      v[1] += a.y;
+      v[2] += a.z;
+      v[3] += a.w;
+      v[4] += b.x;
+      v[5] += b.y;
+      v[6] += b.z;
+      v[7] += b.w;
+    }
+    finish_segment<8>(p.e, m, n, v);
+  }
+}
+
+// ------------------------------------------------------------------ operands
+
+// x = h + m + l: each term takes the leading 8 bits of what is left, truncated, so the three
+// hold the 24 bits of an fp32 value exactly and none overflows (only terms below 2^-133 are
+// lost).  What is not finite goes into h alone.  A bf16 source is copied to rows that TMA can read.
+__global__ void __launch_bounds__(256) muon_pack_kernel(const __grid_constant__ PackParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t groups = p.ld_dst / 8;
+  const int64_t total = groups * p.rows;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t r = i / groups;
+    const int c = static_cast<int>(i - r * groups) * 8;
+    const EpiView src{const_cast<void*>(p.src), p.ld_src, p.src_bf16, p.vec};
+    float x[8];
+    load_segment<8>(src, r * p.ld_src + c, p.cols - c, x);
+    for (int t = 0; t < p.terms; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(x[j]);
+        uint32_t hi = b >> 16;
+        if ((b & 0x7F800000u) == 0x7F800000u) {
+          if (b & 0x007FFFFFu) hi |= 0x40u;  // a NaN stays one
+          x[j] = 0.f;
+        } else {
+          x[j] -= __uint_as_float(b & 0xFFFF0000u);
+        }
+        w[j >> 1] = (j & 1) ? (w[j >> 1] | (hi << 16)) : hi;
+      }
+      *reinterpret_cast<uint4*>(p.dst + t * p.term_stride + r * p.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches
+
+template <class K, class P>
+static cudaError_t launch_dependent(K kernel, const P& p, unsigned blocks, unsigned threads, int smem, int cluster,
+                                    cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <class L>
+static cudaError_t launch_tiles(const ProductParams& p, int sms, cudaStream_t stream) {
+  auto* kernel = muon_product_kernel<L>;
+  static thread_local int configured_device = -1;
+  static thread_local int resident = 0;  // workers (CTAs or pairs) that can run at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    resident = sms / L::CG;
+    if (L::CG == 2) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(sms / 2 * 2, 1, 1);
+      cfg.blockDim = dim3(L::kThreads, 1, 1);
+      cfg.dynamicSmemBytes = L::kSmemBytes;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim = {2, 1, 1};
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      resident = clusters > 0 ? clusters : 1;
+    }
+    configured_device = dev;
+  }
+  const int units = p.tiles_m * p.tiles_n * p.splits;
+  return launch_dependent(kernel, p, static_cast<unsigned>(L::CG * std::min(units, resident)), L::kThreads,
+                          L::kSmemBytes, L::CG, stream);
+}
+
+using Pair256 = Product<2, 256, false, false, false>;
+using Pair256Sum = Product<2, 256, true, false, true>;
+using One128 = Product<1, 128, true, false, false>;
+using Flip32 = Product<1, 32, true, true, false>;
+using Flip64 = Product<1, 64, true, true, false>;
+
+int product_tile_m(int tile) { return tile <= kPair256Sum ? 256 : 128; }
+
+int product_tile_n(int tile) {
+  switch (tile) {
+    case kOne128: return 128;
+    case kFlip32: return 32;
+    case kFlip64: return 64;
+    default: return 256;
+  }
+}
+
+cudaError_t launch_product(int tile, const ProductParams& p, int sms, cudaStream_t stream) {
+  switch (tile) {
+    case kPair256: return launch_tiles<Pair256>(p, sms, stream);
+    case kPair256Sum: return launch_tiles<Pair256Sum>(p, sms, stream);
+    case kOne128: return launch_tiles<One128>(p, sms, stream);
+    case kFlip32: return launch_tiles<Flip32>(p, sms, stream);
+    case kFlip64: return launch_tiles<Flip64>(p, sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+static unsigned loop_blocks(int64_t items, int sms) {
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, 256), int64_t(sms) * 16)));
+}
+
+cudaError_t launch_join(const JoinParams& p, int sms, cudaStream_t stream) {
+  return launch_dependent(muon_join_kernel, p, loop_blocks(ceil_div(p.e.cols, 8) * p.e.rows, sms), 256, 0, 1, stream);
+}
+
+cudaError_t launch_pack(const PackParams& p, int sms, cudaStream_t stream) {
+  return launch_dependent(muon_pack_kernel, p, loop_blocks(p.ld_dst / 8 * p.rows, sms), 256, 0, 1, stream);
+}
+
+}  // namespace muon
+
+extern "C" muon_status_t muon_layers_status(void* stream, int clear, int32_t* device_status, int32_t* where) {
+  if (device_status == nullptr) return MUON_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t h[2] = {0, 0};
+  const int32_t zero[2] = {0, 0};
+  if (cudaMemcpyFromSymbolAsync(h, muon::g_layers_status, sizeof(h), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MUON_ERR_CUDA;
+  if (clear && (cudaMemcpyToSymbolAsync(muon::g_layers_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) !=
+                    cudaSuccess ||
+                cudaStreamSynchronize(s) != cudaSuccess))
+    return MUON_ERR_CUDA;
+  *device_status = h[0];
+  if (where != nullptr) *where = h[1];
+  return MUON_OK;
+}
