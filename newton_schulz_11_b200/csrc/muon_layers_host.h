@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "muon_b200.h"
+#include "muon_product.h"
 
 namespace muon {
 
@@ -94,11 +95,24 @@ inline bool same_view(const muon_view_t& a, const muon_view_t& b, int64_t rows) 
 // Row stride in elements: one row has none of its own.
 inline int64_t row_stride(const muon_view_t& v, int64_t rows, int64_t cols) { return rows <= 1 ? cols : v.ld; }
 
+// A view as the kernels take it, with the widest access its address and row stride allow.
+inline EpiView epi_view(const muon_view_t& v, int64_t rows, int64_t cols) {
+  EpiView e{v.data, row_stride(v, rows, cols), v.dtype == MUON_BF16 ? 1 : 0, 0};
+  const size_t pitch = static_cast<size_t>(e.ld) * elem_bytes(v.dtype);
+  const bool one = rows <= 1;
+  for (int k = 1; k <= 2; ++k)
+    if (aligned_bytes(v.data, 16 * k) && (one || pitch % (16 * k) == 0)) e.vec = k;
+  return e;
+}
+
 // MUON_OK and the SM count when the current device is an sm_100 GPU.
 muon_status_t layers_device(int* sms);
 
 // Device status word of the layer kernels, and the budget of their waits.
 unsigned long long layers_wait_ns();
+
+// Reads (or clears) the status word of the norm kernels, queued on `s`.
+cudaError_t norm_status(int32_t (&out)[2], bool clear, cudaStream_t s);
 
 inline muon_status_t launched() { return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA; }
 

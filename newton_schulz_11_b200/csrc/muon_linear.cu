@@ -109,15 +109,6 @@ bool act_ok(int act) { return act >= MUON_ACT_NONE && act <= MUON_ACT_SILU; }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-EpiView epi_view(const muon_view_t& v, int64_t rows, int64_t cols) {
-  EpiView e{v.data, row_stride(v, rows, cols), v.dtype == MUON_BF16 ? 1 : 0, 0};
-  const size_t pitch = static_cast<size_t>(e.ld) * elem_bytes(v.dtype);
-  const bool one = rows <= 1;
-  for (int k = 1; k <= 2; ++k)
-    if (aligned_bytes(v.data, 16 * k) && (one || pitch % (16 * k) == 0)) e.vec = k;
-  return e;
-}
-
 // An operand of a product: a stored matrix as the tensor cores will read it.
 struct Operand {
   const muon_view_t* v = nullptr;

@@ -621,16 +621,18 @@ cudaError_t launch_pack(const PackParams& p, int sms, cudaStream_t stream) {
 extern "C" muon_status_t muon_layers_status(void* stream, int clear, int32_t* device_status, int32_t* where) {
   if (device_status == nullptr) return MUON_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int32_t h[2] = {0, 0};
+  int32_t product[2] = {0, 0}, norm[2] = {0, 0};
   const int32_t zero[2] = {0, 0};
-  if (cudaMemcpyFromSymbolAsync(h, muon::g_layers_status, sizeof(h), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
+  if (cudaMemcpyFromSymbolAsync(product, muon::g_layers_status, sizeof(product), 0, cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      muon::norm_status(norm, false, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
     return MUON_ERR_CUDA;
   if (clear && (cudaMemcpyToSymbolAsync(muon::g_layers_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) !=
                     cudaSuccess ||
-                cudaStreamSynchronize(s) != cudaSuccess))
+                muon::norm_status(norm, true, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess))
     return MUON_ERR_CUDA;
-  *device_status = h[0];
-  if (where != nullptr) *where = h[1];
+  const int32_t* first = product[0] != 0 ? product : norm;
+  *device_status = first[0];
+  if (where != nullptr) *where = first[1];
   return MUON_OK;
 }
