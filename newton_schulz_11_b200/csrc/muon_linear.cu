@@ -148,7 +148,7 @@ int segments(int ta, int tb) { return ta == 1 ? tb : (tb == 1 ? ta : kMaxSegment
 // Picks the tile and the number of splits with the least estimated time, in SM cycles:
 // waves of units times their k-blocks, and for a join the partial sums' way out and back.
 // sum: some output is fp32.  raw: the epilogue does no more than add and store fp32.
-Plan make_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, bool may_flip) {
+Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, bool may_flip) {
   Plan best;
   double least = 1e30;
   const int64_t nk = ceil_div(k, kProductBK);
@@ -186,6 +186,30 @@ Plan make_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, bo
     best.partial_bytes = up(static_cast<size_t>(best.splits) * m * best.ld_partial * 4);
   }
   return best;
+}
+
+// The search takes a microsecond or two; a call asks for its plan twice (its workspace, then
+// itself), and a training loop for the same few sizes again and again.
+Plan make_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, bool may_flip) {
+  struct Entry {
+    int64_t m = -1, n = 0, k = 0;
+    int flags = 0;
+    Plan plan;
+  };
+  static thread_local Entry table[64];
+  const int flags = nseg * 8 + (sum ? 4 : 0) + (raw ? 2 : 0) + (may_flip ? 1 : 0);
+  uint64_t h = static_cast<uint64_t>(m) * 0x9E3779B97F4A7C15ull;
+  h = (h ^ static_cast<uint64_t>(n)) * 0x9E3779B97F4A7C15ull;
+  h = (h ^ static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull;
+  Entry& e = table[((h >> 32) ^ static_cast<uint64_t>(flags)) % 64];
+  if (e.m != m || e.n != n || e.k != k || e.flags != flags) {
+    e.plan = search_plan(m, n, k, nseg, sum, raw, may_flip);
+    e.m = m;
+    e.n = n;
+    e.k = k;
+    e.flags = flags;
+  }
+  return e.plan;
 }
 
 muon_status_t pack(const Operand& o, uint8_t* ws, cudaStream_t s) {

@@ -24,6 +24,10 @@ from ._lib import MUON_ACTS, check, lib
 _CODES = {torch.float32: _lib.MUON_F32, torch.bfloat16: _lib.MUON_BF16}
 _ABSENT = (None, 0, 0, 0)
 _byref = ctypes.byref
+# Short calls are bound by this file's host time, so the current device and stream are asked
+# for without building Python objects (0.2 us for both, against 2.4 us).
+_device_index = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _matrix(t, what: str, rows: int, cols: int, device, dtype=None):
@@ -86,13 +90,16 @@ def _elsewhere(device, stream):
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    if _device_index() != device.index:
         return torch.cuda.device(device)
     return None
 
 
-def _current(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _new(like: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
+    """An uninitialised rows x cols matrix of like's dtype, on its device."""
+    if like.is_contiguous() and like.shape == (rows, cols):
+        return torch.empty_like(like)
+    return like.new_empty((rows, cols))
 
 
 def _scratch(size_fn, desc, workspace, device, stream: int):
@@ -125,15 +132,15 @@ def layer_norm(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias: Optio
         with ctx:
             return layer_norm(x, gain, bias, eps=eps, out=out)
     if out is None:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=device)
-    stats = torch.empty((2, rows), dtype=torch.float32, device=device)
-    mean, rstd = stats[0], stats[1]
+        out = _new(x, rows, cols)
+    mean = x.new_empty(rows, dtype=torch.float32)
+    rstd = torch.empty_like(mean)
     d = _lib.MuonLayerNorm(*_matrix(x, "x", rows, cols, device),
                            *(_ABSENT if gain is None else _vector(gain, "gain", cols, device)),
                            *(_ABSENT if bias is None else _vector(bias, "bias", cols, device)),
                            *_matrix(out, "out", rows, cols, device, x.dtype),
                            mean.data_ptr(), rstd.data_ptr(), rows, cols, eps, 0)
-    st = lib().muon_layer_norm(_byref(d), _current(device))
+    st = lib().muon_layer_norm(_byref(d), _raw_stream(device.index))
     if st:
         check(st, "muon_layer_norm")
     return out, mean, rstd
@@ -161,11 +168,11 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
         raise ValueError("accumulate needs dgain and dbias")
     f32 = torch.float32
     if dx is None:
-        dx = torch.empty((rows, cols), dtype=x.dtype, device=device)
+        dx = _new(x, rows, cols)
     if dgain is None:
-        dgain = torch.empty(cols, dtype=f32, device=device)
+        dgain = x.new_empty(cols, dtype=f32)
     if dbias is None:
-        dbias = torch.empty(cols, dtype=f32, device=device)
+        dbias = x.new_empty(cols, dtype=f32)
     d = _lib.MuonLayerNormGrad(*_matrix(dy, "dy", rows, cols, device, x.dtype),
                                *_matrix(x, "x", rows, cols, device),
                                *(_ABSENT if gain is None else _vector(gain, "gain", cols, device)),
@@ -175,7 +182,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                                _vector(rstd, "rstd", rows, device, f32)[0],
                                _vector(dgain, "dgain", cols, device, f32)[0],
                                _vector(dbias, "dbias", cols, device, f32)[0], rows, cols, 1 if accumulate else 0, 0)
-    h, s = lib(), _current(device)
+    h, s = lib(), _raw_stream(device.index)
     ptr, size, _keep = _scratch(h.muon_layer_norm_backward_workspace, d, workspace, device, s)
     st = h.muon_layer_norm_backward(_byref(d), ptr, size, s)
     if st:
@@ -204,16 +211,16 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     code = _act_code(act)
     xv = _matrix(x, "x", rows, n_in, device)
     if out is None:
-        out = torch.empty((rows, n_out), dtype=x.dtype, device=device)
+        out = _new(x, rows, n_out)
     if save_preact and preact is None:
-        preact = torch.empty((rows, n_out), dtype=x.dtype, device=device)
+        preact = _new(x, rows, n_out)
     d = _lib.MuonLinear(*xv, *_matrix(w, "w", n_out, n_in, device),
                         *(_ABSENT if bias is None else _vector(bias, "bias", n_out, device)),
                         *(_ABSENT if residual is None else _matrix(residual, "residual", rows, n_out, device)),
                         *_matrix(out, "out", rows, n_out, device),
                         *(_ABSENT if preact is None else _matrix(preact, "preact", rows, n_out, device)),
                         rows, n_in, n_out, code, 0)
-    h, s = lib(), _current(device)
+    h, s = lib(), _raw_stream(device.index)
     ptr, size, _keep = _scratch(h.muon_linear_workspace, d, workspace, device, s)
     st = h.muon_linear(_byref(d), ptr, size, s)
     if st:
@@ -258,15 +265,15 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, in_ac
     if not need_dx:
         dx = None
     elif dx is None:
-        dx = torch.empty((rows, n_in), dtype=dy.dtype, device=device)
+        dx = _new(dy, rows, n_in)
     if not need_dw:
         dw = None
     elif dw is None:
-        dw = torch.empty((n_out, n_in), dtype=f32, device=device)
+        dw = dy.new_empty((n_out, n_in), dtype=f32)
     if not need_db:
         db = None
     elif db is None:
-        db = torch.empty(n_out, dtype=f32, device=device)
+        db = dy.new_empty(n_out, dtype=f32)
     d = _lib.MuonLinearGrad(*dyv, *_matrix(x, "x", rows, n_in, device), *_matrix(w, "w", n_out, n_in, device),
                             *(_ABSENT if in_preact is None or not code
                               else _matrix(in_preact, "in_preact", rows, n_in, device)),
@@ -275,7 +282,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, in_ac
                             *(_ABSENT if dw is None else _matrix(dw, "dw", n_out, n_in, device, f32)),
                             None if db is None else _vector(db, "db", n_out, device, f32)[0],
                             rows, n_in, n_out, code, 1 if accumulate else 0)
-    h, s = lib(), _current(device)
+    h, s = lib(), _raw_stream(device.index)
     ptr, size, _keep = _scratch(h.muon_linear_backward_workspace, d, workspace, device, s)
     st = h.muon_linear_backward(_byref(d), ptr, size, s)
     if st:
@@ -296,10 +303,10 @@ def activation_backward(dy: torch.Tensor, preact: torch.Tensor, act: str, *, out
         raise ValueError("act must name an activation")
     dyv = _matrix(dy, "dy", rows, cols, device)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dy.dtype, device=device)
+        out = _new(dy, rows, cols)
     d = _lib.MuonActivationGrad(*dyv, *_matrix(preact, "preact", rows, cols, device),
                                 *_matrix(out, "out", rows, cols, device, dy.dtype), rows, cols, code, 0)
-    st = lib().muon_activation_backward(_byref(d), _current(device))
+    st = lib().muon_activation_backward(_byref(d), _raw_stream(device.index))
     if st:
         check(st, "muon_activation_backward")
     return out
@@ -313,6 +320,6 @@ def layers_status(device=None, *, clear: bool = False, stream=None) -> Tuple[int
         device = torch.device("cuda", torch.cuda.current_device())
     code, where = ctypes.c_int32(0), ctypes.c_int32(0)
     with torch.cuda.device(device):
-        s = _current(device) if stream is None else stream.cuda_stream
+        s = _raw_stream(device.index) if stream is None else stream.cuda_stream
         check(lib().muon_layers_status(s, 1 if clear else 0, _byref(code), _byref(where)), "muon_layers_status")
     return int(code.value), int(where.value)
