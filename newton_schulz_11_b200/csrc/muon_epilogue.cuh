@@ -135,7 +135,120 @@ __device__ __forceinline__ void apply_slope(int act, const float (&t)[NC], float
 #undef MUON_EACH
 }
 
-// Row m, columns [n, n + NC) of the output (n a multiple of 8), from the sums in v.
+// ------------------------------------------------------------------ the common epilogue
+//
+// When everything but the bias is bf16 in rows of whole 32-byte units, 32 columns of a row
+// are 64 bytes of each operand.  With two epilogue warps per scheduler, the epilogue's pace
+// is its number of instructions times their latency, so this path has no choices inside:
+// addresses are carried per row, and the inputs are fetched a step ahead (16 words each).
+struct EpiRow {
+  const uint8_t* slope;
+  const uint8_t* add;
+  uint8_t* preact;
+  uint8_t* out;
+  uint32_t slope_w[16], add_w[16];
+
+  __device__ __forceinline__ void start(const Epilogue& e, int64_t m, int64_t n) {
+    slope = e.slope.p == nullptr ? nullptr : static_cast<const uint8_t*>(e.slope.p) + 2 * (m * e.slope.ld + n);
+    add = e.add.p == nullptr ? nullptr : static_cast<const uint8_t*>(e.add.p) + 2 * (m * e.add.ld + n);
+    preact = e.preact.p == nullptr ? nullptr : static_cast<uint8_t*>(e.preact.p) + 2 * (m * e.preact.ld + n);
+    out = static_cast<uint8_t*>(e.out.p) + 2 * (m * e.out.ld + n);
+  }
+
+  static __device__ __forceinline__ void words(const uint8_t* p, uint32_t (&w)[16]) {
+    uint4 a, b, c, d;
+    ld_global_v8(p, a, b);
+    ld_global_v8(p + 32, c, d);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    w[8] = c.x, w[9] = c.y, w[10] = c.z, w[11] = c.w, w[12] = d.x, w[13] = d.y, w[14] = d.z, w[15] = d.w;
+  }
+
+  __device__ __forceinline__ void fetch(int col) {
+    if (slope != nullptr) words(slope + 2 * col, slope_w);
+    if (add != nullptr) words(add + 2 * col, add_w);
+  }
+
+  static __device__ __forceinline__ void store(uint8_t* p, const F2 (&v)[16]) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float2 f = split(v[j]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    st_global_v8(p, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+    st_global_v8(p + 32, make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
+  }
+
+  // Columns [col, col + 32) of the row (from column n of the output), from the sums in v;
+  // `more`: the next 32 follow.
+  __device__ __forceinline__ void finish(const Epilogue& e, int64_t n, int col, bool more, F2 (&v)[16]) {
+    if (e.bias.p != nullptr) {
+      if (e.bias.bf16) {
+        uint32_t w[16];
+        words(static_cast<const uint8_t*>(e.bias.p) + 2 * n, w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          v[j] = add2(v[j], pair(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)));
+      } else {
+        const float* b = static_cast<const float*>(e.bias.p) + n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 x, y;
+          ld_global_v8(b + 8 * j, x, y);
+          v[4 * j] = add2(v[4 * j], pair(__uint_as_float(x.x), __uint_as_float(x.y)));
+          v[4 * j + 1] = add2(v[4 * j + 1], pair(__uint_as_float(x.z), __uint_as_float(x.w)));
+          v[4 * j + 2] = add2(v[4 * j + 2], pair(__uint_as_float(y.x), __uint_as_float(y.y)));
+          v[4 * j + 3] = add2(v[4 * j + 3], pair(__uint_as_float(y.z), __uint_as_float(y.w)));
+        }
+      }
+    }
+    if (preact != nullptr) store(preact + 2 * col, v);
+    if (e.act != MUON_ACT_NONE) {
+      float x[32];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float2 f = split(v[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+      }
+      apply_act<32>(e.act, x);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = pair(x[2 * j], x[2 * j + 1]);
+    }
+    if (slope != nullptr) {
+      float t[32], x[32];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float2 f = split(v[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+        t[2 * j] = __uint_as_float(slope_w[j] << 16);
+        t[2 * j + 1] = __uint_as_float(slope_w[j] & 0xFFFF0000u);
+      }
+      apply_slope<32>(e.slope_act, t, x);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = pair(x[2 * j], x[2 * j + 1]);
+    }
+    if (add != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        v[j] = add2(v[j], pair(__uint_as_float(add_w[j] << 16), __uint_as_float(add_w[j] & 0xFFFF0000u)));
+    }
+    if (more) fetch(col + 32);
+    store(out + 2 * col, v);
+  }
+};
+
+// Brings `cols` columns of row m from column n on into L2.
+__device__ __forceinline__ void prefetch_row(const EpiView& v, int64_t m, int64_t n, int cols) {
+  if (v.p == nullptr) return;
+  const int step = v.bf16 ? 64 : 32;  // 128 bytes
+  const char* p = static_cast<const char*>(v.p) + (m * v.ld + n) * (v.bf16 ? 2 : 4);
+  for (int c = 0; c < cols; c += step) prefetch_l2(p + c * (v.bf16 ? 2 : 4));
+}
+
+// Row m, columns [n, n + NC) (n a multiple of 8) without a fetch ahead: the join kernel's.
 template <int NC>
 __device__ __forceinline__ void finish_segment(const Epilogue& e, int64_t m, int64_t n, float (&v)[NC]) {
   const int64_t left = e.cols - n;

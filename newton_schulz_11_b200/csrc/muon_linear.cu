@@ -53,18 +53,31 @@ __global__ void __launch_bounds__(256) muon_column_sum_kernel(const __grid_const
   if (o < p.cols) {
     float t = red[0][threadIdx.x];
     for (int k = 1; k < 8; ++k) t += red[k][threadIdx.x];
-    p.partial[blockIdx.y * p.ld_partial + o] = t;
+    if (p.slices == 1)
+      p.db[o] = p.accumulate ? p.db[o] + t : t;
+    else
+      p.partial[blockIdx.y * p.ld_partial + o] = t;
   }
 }
 
+// 32 columns per block, 8 warps over the slices.
 __global__ void __launch_bounds__(256) muon_column_join_kernel(const __grid_constant__ ColumnSumParams p) {
+  __shared__ float red[8][32];
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.cols) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float t = 0.f;
-  for (int s = 0; s < p.slices; ++s) t += p.partial[s * p.ld_partial + c];
-  p.db[c] = p.accumulate ? p.db[c] + t : t;
+  if (c < p.cols) {
+#pragma unroll 4
+    for (int s = w; s < p.slices; s += 8) t += p.partial[s * p.ld_partial + c];
+  }
+  red[w][lane] = t;
+  __syncthreads();
+  if (w == 0 && c < p.cols) {
+    for (int k = 1; k < 8; ++k) t += red[k][lane];
+    p.db[c] = p.accumulate ? p.db[c] + t : t;
+  }
 }
 
 struct ActGradParams {
@@ -138,7 +151,6 @@ struct Plan {
   int tile = kOne128;
   int64_t tiles_m = 0, tiles_n = 0, nk = 0, splits = 1, kb_per_split = 0;
   int nseg = 1;
-  bool join = false;  // through partial sums and the join kernel
   size_t partial_bytes = 0;
   int64_t ld_partial = 0;
 };
@@ -146,9 +158,9 @@ struct Plan {
 int segments(int ta, int tb) { return ta == 1 ? tb : (tb == 1 ? ta : kMaxSegments); }
 
 // Picks the tile and the number of splits with the least estimated time, in SM cycles:
-// waves of units times their k-blocks, and for a join the partial sums' way out and back.
-// sum: some output is fp32.  raw: the epilogue does no more than add and store fp32.
-Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, bool may_flip) {
+// waves of units times their k-blocks, and for a split the partial sums' way out and back.
+// sum: some output is fp32.
+Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool may_flip) {
   Plan best;
   double least = 1e30;
   const int64_t nk = ceil_div(k, kProductBK);
@@ -166,8 +178,7 @@ Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, 
       if (splits != want || (want > 1 && per < 2) || tm * tn * splits > 0x3fffffff) continue;
       const double waves = static_cast<double>(ceil_div(tm * tn * splits, workers));
       double cost = waves * (per * block + 600.0) + 3000.0;
-      const bool join = splits > 1 || (tile == kPair256Sum && !raw);
-      if (join) cost += 3500.0 + static_cast<double>(splits + 1) * m * n * 4.0 / 3000.0;
+      if (splits > 1) cost += 3500.0 + static_cast<double>(splits + 1) * m * n * 4.0 / 3000.0;
       if (cost < least) {
         least = cost;
         best.tile = tile;
@@ -175,13 +186,12 @@ Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, 
         best.tiles_n = tn;
         best.splits = splits;
         best.kb_per_split = per;
-        best.join = join;
       }
     }
   }
   best.nk = nk;
   best.nseg = nseg;
-  if (best.join) {
+  if (best.splits > 1) {
     best.ld_partial = ceil_div(n, 32) * 32;
     best.partial_bytes = up(static_cast<size_t>(best.splits) * m * best.ld_partial * 4);
   }
@@ -190,20 +200,20 @@ Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, 
 
 // The search takes a microsecond or two; a call asks for its plan twice (its workspace, then
 // itself), and a training loop for the same few sizes again and again.
-Plan make_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool raw, bool may_flip) {
+Plan make_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool may_flip) {
   struct Entry {
     int64_t m = -1, n = 0, k = 0;
     int flags = 0;
     Plan plan;
   };
   static thread_local Entry table[64];
-  const int flags = nseg * 8 + (sum ? 4 : 0) + (raw ? 2 : 0) + (may_flip ? 1 : 0);
+  const int flags = nseg * 4 + (sum ? 2 : 0) + (may_flip ? 1 : 0);
   uint64_t h = static_cast<uint64_t>(m) * 0x9E3779B97F4A7C15ull;
   h = (h ^ static_cast<uint64_t>(n)) * 0x9E3779B97F4A7C15ull;
   h = (h ^ static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull;
   Entry& e = table[((h >> 32) ^ static_cast<uint64_t>(flags)) % 64];
   if (e.m != m || e.n != n || e.k != k || e.flags != flags) {
-    e.plan = search_plan(m, n, k, nseg, sum, raw, may_flip);
+    e.plan = search_plan(m, n, k, nseg, sum, may_flip);
     e.m = m;
     e.n = n;
     e.k = k;
@@ -239,6 +249,12 @@ bool operand_maps(CUtensorMap* maps, const Operand& o, uint8_t* ws, bool mn, int
   return true;
 }
 
+bool plain_epilogue(const Epilogue& e) {
+  for (const EpiView* v : {&e.preact, &e.slope, &e.add, &e.out})
+    if (v->p != nullptr && !(v->bf16 && v->vec == 2)) return false;
+  return e.bias.p == nullptr || e.bias.vec == 2;
+}
+
 // a: the operand on the output's row side; b: on its column side.  mn: contiguous along the side.
 muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const Epilogue& e,
                           uint8_t* ws, size_t partial_at, cudaStream_t s) {
@@ -252,6 +268,7 @@ muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Ope
       !operand_maps(p.map_b, bm, ws, p.b_mn, pl.tile <= kPair256Sum ? 128 : product_tile_n(pl.tile)))
     return MUON_ERR_CUDA;
   p.e = e;
+  p.e.plain = plain_epilogue(e);
   p.tiles_m = static_cast<int32_t>(pl.tiles_m);
   p.tiles_n = static_cast<int32_t>(pl.tiles_n);
   p.nk = static_cast<int32_t>(pl.nk);
@@ -264,13 +281,13 @@ muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Ope
     p.seg_b[g] = static_cast<uint8_t>(bm.terms == 1 ? 0 : am.terms == 1 ? pl.nseg - 1 - g : both_b[g]);
   }
   p.timeout_ns = layers_wait_ns();
-  if (pl.join) {
+  if (pl.splits > 1) {
     p.partial = reinterpret_cast<float*>(ws + partial_at);
     p.ld_partial = pl.ld_partial;
     p.split_stride = e.rows * pl.ld_partial;
   }
   if (launch_product(pl.tile, p, kSms, s) != cudaSuccess) return MUON_ERR_CUDA;
-  if (pl.join) {
+  if (pl.splits > 1) {
     JoinParams j{};
     j.e = e;
     j.partial = p.partial;
@@ -296,7 +313,7 @@ LinearPlan plan_linear(const muon_linear_t* d) {
   pl.x = Operand(d->x, d->rows, d->in);
   pl.w = Operand(d->w, d->out, d->in);
   pl.z = make_plan(d->rows, d->out, d->in, segments(pl.x.terms, pl.w.terms), wants_sum(d->y) || wants_sum(d->preact),
-                   false, true);
+                   true);
   pl.x.place(&pl.bytes);
   pl.w.place(&pl.bytes);
   pl.partial_at = pl.bytes;
@@ -321,21 +338,21 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
   if (dx) {
     pl.w = Operand(d->w, d->out, d->in);
     pl.w.place(&pl.bytes);
-    pl.dx = make_plan(d->rows, d->in, d->out, segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), false, true);
+    pl.dx = make_plan(d->rows, d->in, d->out, segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), true);
     partial = pl.dx.partial_bytes;
   }
   if (dw) {
     pl.x = Operand(d->x, d->rows, d->in);
     pl.x.place(&pl.bytes);
-    pl.dw = make_plan(d->out, d->in, d->rows, segments(pl.dy.terms, pl.x.terms), true, true, false);
+    pl.dw = make_plan(d->out, d->in, d->rows, segments(pl.dy.terms, pl.x.terms), true, false);
     partial = std::max(partial, pl.dw.partial_bytes);  // the products run one after the other
   }
   pl.partial_at = pl.bytes;
   pl.bytes += partial;
   if (d->db != nullptr) {
-    pl.slices = std::max<int64_t>(1, std::min(ceil_div(d->rows, 64), 4 * kSms / ceil_div(d->out, 256)));
+    pl.slices = std::max<int64_t>(1, std::min(d->rows / 128, 4 * kSms / ceil_div(d->out, 256)));
     pl.db_at = pl.bytes;
-    pl.bytes += up(static_cast<size_t>(pl.slices) * d->out * 4);
+    if (pl.slices > 1) pl.bytes += up(static_cast<size_t>(pl.slices) * d->out * 4);
   }
   return pl;
 }
@@ -500,7 +517,7 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     c.slices = static_cast<int32_t>(pl.slices);
     const unsigned blocks = static_cast<unsigned>(ceil_div(d->out, 256));
     if ((st = launch_after(muon_column_sum_kernel, c, dim3(blocks, c.slices), s)) != MUON_OK) return st;
-    return launch_after(muon_column_join_kernel, c, dim3(blocks), s);
+    if (c.slices > 1) return launch_after(muon_column_join_kernel, c, dim3(static_cast<unsigned>(ceil_div(d->out, 32))), s);
   }
   return MUON_OK;
 }

@@ -62,15 +62,26 @@ __device__ __forceinline__ void tmem_load_row(uint32_t taddr, uint32_t (&v)[NC])
   tmem_wait_ld();
 }
 
+// 16 columns of this thread's lane, written.
+__device__ __forceinline__ void tmem_store_row16(uint32_t taddr, const float* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(x[8]), "f"(x[9]),
+      "f"(x[10]), "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), "f"(x[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Per-CTA layout of a variant.  CG CTAs share a tile of 128 CG x TN; each stages its own 128
 // rows of A and TN / CG rows of B, 64 deep.
 // SUM: the reduction in pieces added in registers.  FLIP: the tile's rows are the output's
-// columns.  RAW: the epilogue only adds and stores fp32 (a pair's 128 sums a thread leave no
-// registers for more; what needs more goes through partial sums and the join kernel).
-template <int CG_, int TN_, bool SUM_, bool FLIP_, bool RAW_>
+// columns.
+template <int CG_, int TN_, bool SUM_, bool FLIP_>
 struct Product {
   static constexpr int CG = CG_, TM = 128 * CG_, TN = TN_, TNB = TN_ / CG_;
-  static constexpr bool SUM = SUM_, FLIP = FLIP_, RAW = RAW_;
+  static constexpr bool SUM = SUM_, FLIP = FLIP_;
   static constexpr int BK = kProductBK;
   static constexpr int kABytes = 128 * BK * 2;
   static constexpr int kBBytes = TNB * BK * 2;
@@ -81,9 +92,10 @@ struct Product {
   static constexpr int NEPI = 8;              // epilogue warps
   static constexpr int kThreads = 64 + 32 * NEPI;
   static constexpr int NCW = TN / 2;          // accumulator columns per epilogue thread
-  static constexpr int NC = SUM ? 16 : 32;                // read from tensor memory at a time
-  static constexpr int FC = FLIP ? 16 : SUM ? 8 : 32;     // finished at a time
+  static constexpr int NC = NCW < 32 ? NCW : 32;  // finished at a time
   static constexpr int kTmemCols = 2 * TN;
+  // whether the common epilogue can come up: a pair that sums has an fp32 output
+  static constexpr bool kPlain = !FLIP && !(SUM && CG == 2);
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
   static_assert((2 * S + 5) * 8 + 16 <= 256, "barrier area");
@@ -356,89 +368,101 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
       const Unit u = decode_unit(p, t);
       const int64_t row = static_cast<int64_t>(L::TM) * u.i + 128 * rank + r;
       const int64_t col = static_cast<int64_t>(TN) * u.j + h * L::NCW;
-      float sum[L::SUM ? L::NCW : 1];
-#pragma unroll
-      for (int j = 0; j < (L::SUM ? L::NCW : 1); ++j) sum[j] = 0.f;
-      for (int pb = u.kb0; pb < u.kb1; pb += p.piece) {
+      float* part = p.partial == nullptr ? nullptr : p.partial + u.split * p.split_stride;
+      EpiRow at;
+      // the common epilogue, where all of the warp's rows and columns exist
+      const bool plain =
+          L::kPlain && p.e.plain && part == nullptr && row - lane + 32 <= p.e.rows && col + L::NCW <= p.e.cols;
+      if constexpr (!L::FLIP) {  // the epilogue's inputs move while the tile's products run
+        if (plain) at.start(p.e, row, col);
+        if (part == nullptr && row < p.e.rows && col < p.e.cols) {
+          const int width = p.e.cols - col < L::NCW ? static_cast<int>(p.e.cols - col) : L::NCW;
+          prefetch_row(p.e.slope, row, col, width);
+          prefetch_row(p.e.add, row, col, width);
+        }
+        if constexpr (L::kPlain && !L::SUM) {
+          if (plain) at.fetch(0);
+        }
+      }
+      uint32_t tacc = 0;
+      auto await = [&]() {
+        __syncwarp();
         ok = warp_waits(&tfull[acc], aph, wd, kSiteAccReady);
-        if (!ok) break;
         tc_fence_after();
-        const uint32_t tacc = tmem_base + static_cast<uint32_t>(acc * TN + h * L::NCW) +
-                              (static_cast<uint32_t>(q4 * 32) << 16);
-        if constexpr (L::SUM) {
-#pragma unroll
-          for (int c = 0; c < L::NCW; c += NC) {
-            uint32_t v[NC];
-            tmem_load_row<NC>(tacc + c, v);
-#pragma unroll
-            for (int j = 0; j < NC; ++j) sum[c + j] += __uint_as_float(v[j]);
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < L::NCW; c += NC) {
-            uint32_t v[NC];
-            tmem_load_row<NC>(tacc + c, v);
-            float x[NC];
-#pragma unroll
-            for (int j = 0; j < NC; ++j) x[j] = __uint_as_float(v[j]);
-            if (c + NC == L::NCW) {  // the last read: the accumulator is free
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8u * static_cast<uint32_t>(acc));
-            }
-            if (p.partial != nullptr) {
-              const EpiView out{p.partial + u.split * p.split_stride, p.ld_partial, 0, 2};
-              if (row < p.e.rows && col + c < p.ld_partial) store_segment<NC>(out, row * out.ld + col + c, NC, x);
-            } else {
-              finish_segment<NC>(p.e, row, col + c, x);
-            }
-          }
-        }
-        if constexpr (L::SUM) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8u * static_cast<uint32_t>(acc));
-        }
+        tacc = tmem_base + static_cast<uint32_t>(acc * TN + h * L::NCW) + (static_cast<uint32_t>(q4 * 32) << 16);
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8u * static_cast<uint32_t>(acc));
         if (++acc == 2) {
           acc = 0;
           aph ^= 1u;
         }
-      }
+      };
+      await();
       if constexpr (L::SUM) {
-        if (!ok) break;
-        constexpr int FC = L::FC;
-        float* part = p.partial == nullptr ? nullptr : p.partial + u.split * p.split_stride;
+        if (u.kb1 - u.kb0 > p.piece) {
+          // Pieces are added in registers; the whole sum goes back to the last piece's
+          // columns, so that the code below finds it where a single piece would be.
+          float sum[L::NCW];
 #pragma unroll
-        for (int c = 0; c < L::NCW; c += FC) {
-          float x[FC];
+          for (int j = 0; j < L::NCW; ++j) sum[j] = 0.f;
+          for (int pb = u.kb0; ok;) {
 #pragma unroll
-          for (int j = 0; j < FC; ++j) x[j] = sum[c + j];
-          if (part != nullptr) {
-            if constexpr (L::FLIP) {  // row: a feature; col: the first of FC tokens
+            for (int c = 0; c < L::NCW; c += 16) {
+              uint32_t v[16];
+              tmem_load_row<16>(tacc + c, v);
 #pragma unroll
-              for (int j = 0; j < FC; ++j)
-                if (row < p.e.cols && col + c + j < p.e.rows) part[(col + c + j) * p.ld_partial + row] = x[j];
-            } else {
-              const EpiView out{part, p.ld_partial, 0, 2};
-              if (row < p.e.rows && col + c < p.ld_partial) store_segment<FC>(out, row * out.ld + col + c, FC, x);
+              for (int j = 0; j < 16; ++j) sum[c + j] += __uint_as_float(v[j]);
             }
-          } else if constexpr (L::RAW) {
-            const int64_t left = p.e.cols - col - c;
-            if (row < p.e.rows && left > 0) {
-              const int valid = left < FC ? static_cast<int>(left) : FC;
-              if (p.e.add.p != nullptr) {
-                float a[FC];
-                load_segment<FC>(p.e.add, row * p.e.add.ld + col + c, valid, a);
-#pragma unroll
-                for (int j = 0; j < FC; ++j) x[j] += a[j];
-              }
-              store_segment<FC>(p.e.out, row * p.e.out.ld + col + c, valid, x);
-            }
-          } else if constexpr (L::FLIP) {
-            finish_column<FC>(p.e, col + c, row, x);
-          } else {
-            finish_segment<FC>(p.e, row, col + c, x);
+            pb += p.piece;
+            if (pb >= u.kb1) break;
+            release();
+            await();
           }
+          if (ok) {
+#pragma unroll
+            for (int c = 0; c < L::NCW; c += 16) tmem_store_row16(tacc + c, &sum[c]);
+            tmem_wait_st();
+          }
+        }
+        if constexpr (L::kPlain) {
+          if (plain) at.fetch(0);
+        }
+      }
+      if (!ok) break;
+#pragma unroll 1
+      for (int c = 0; c < L::NCW; c += NC) {
+        uint32_t v[NC];
+        __syncwarp();  // lanes may have parted over edges
+        tmem_load_row<NC>(tacc + c, v);
+        if (c + NC == L::NCW) release();  // the last read
+        if constexpr (L::kPlain) {
+          if (plain) {
+            F2 x[NC / 2];
+#pragma unroll
+            for (int j = 0; j < NC / 2; ++j) x[j] = pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            at.finish(p.e, col + c, c, c + NC < L::NCW, x);
+            continue;
+          }
+        }
+        float x[NC];
+#pragma unroll
+        for (int j = 0; j < NC; ++j) x[j] = __uint_as_float(v[j]);
+        if constexpr (L::FLIP) {  // row: a feature; col: the first of NC tokens
+          if (part != nullptr) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+              if (row < p.e.cols && col + c + j < p.e.rows) part[(col + c + j) * p.ld_partial + row] = x[j];
+          } else {
+            finish_column<NC>(p.e, col + c, row, x);
+          }
+        } else if (part != nullptr) {
+          const EpiView out{part, p.ld_partial, 0, 2};
+          if (row < p.e.rows && col + c < p.ld_partial) store_segment<NC>(out, row * out.ld + col + c, NC, x);
+        } else {
+          finish_segment<NC>(p.e, row, col + c, x);
         }
       }
     }
@@ -576,11 +600,11 @@ static cudaError_t launch_tiles(const ProductParams& p, int sms, cudaStream_t st
                           L::kSmemBytes, L::CG, stream);
 }
 
-using Pair256 = Product<2, 256, false, false, false>;
-using Pair256Sum = Product<2, 256, true, false, true>;
-using One128 = Product<1, 128, true, false, false>;
-using Flip32 = Product<1, 32, true, true, false>;
-using Flip64 = Product<1, 64, true, true, false>;
+using Pair256 = Product<2, 256, false, false>;
+using Pair256Sum = Product<2, 256, true, false>;
+using One128 = Product<1, 128, true, false>;
+using Flip32 = Product<1, 32, true, true>;
+using Flip64 = Product<1, 64, true, true>;
 
 int product_tile_m(int tile) { return tile <= kPair256Sum ? 256 : 128; }
 

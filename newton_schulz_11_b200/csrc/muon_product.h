@@ -24,6 +24,7 @@ struct Epilogue {
   EpiView bias, preact, slope, add, out;
   int64_t rows, cols;  // of the output
   int32_t act, slope_act;
+  int32_t plain;  // all but the bias bf16, in rows of whole 32-byte units; a 32-byte aligned bias
 };
 
 constexpr int kTerms = 3;                // bf16 terms of an fp32 operand
