@@ -100,53 +100,41 @@ __device__ __forceinline__ void store_segment(const EpiView& v, int64_t off, int
   }
 }
 
-// v = act(v) and v *= act'(t), the choice made once for the segment.
 template <int NC>
-__device__ __forceinline__ void apply_act(int act, float (&v)[NC]) {
-#define MUON_EACH(A)                                        \
-  case A:                                                   \
-    _Pragma("unroll") for (int j = 0; j < NC; ++j) v[j] = act_value(A, v[j]); \
-    break
-  switch (act) {
-    MUON_EACH(MUON_ACT_RELU);
-    MUON_EACH(MUON_ACT_RELU2);
-    MUON_EACH(MUON_ACT_GELU);
-    MUON_EACH(MUON_ACT_GELU_TANH);
-    MUON_EACH(MUON_ACT_SILU);
-    default: break;
-  }
-#undef MUON_EACH
+__device__ __forceinline__ void load_pairs(const EpiView& v, int64_t off, int valid, F2 (&x)[NC / 2]) {
+  float e[NC];
+  load_segment<NC>(v, off, valid, e);
+#pragma unroll
+  for (int j = 0; j < NC / 2; ++j) x[j] = pair(e[2 * j], e[2 * j + 1]);
 }
 
 template <int NC>
-__device__ __forceinline__ void apply_slope(int act, const float (&t)[NC], float (&v)[NC]) {
-#define MUON_EACH(A)                                        \
-  case A:                                                   \
-    _Pragma("unroll") for (int j = 0; j < NC; ++j) v[j] *= act_slope(A, t[j]); \
-    break
-  switch (act) {
-    MUON_EACH(MUON_ACT_RELU);
-    MUON_EACH(MUON_ACT_RELU2);
-    MUON_EACH(MUON_ACT_GELU);
-    MUON_EACH(MUON_ACT_GELU_TANH);
-    MUON_EACH(MUON_ACT_SILU);
-    default: break;
+__device__ __forceinline__ void store_pairs(const EpiView& v, int64_t off, int valid, const F2 (&x)[NC / 2]) {
+  float e[NC];
+#pragma unroll
+  for (int j = 0; j < NC / 2; ++j) {
+    const float2 f = split(x[j]);
+    e[2 * j] = f.x;
+    e[2 * j + 1] = f.y;
   }
-#undef MUON_EACH
+  store_segment<NC>(v, off, valid, e);
 }
 
 // ------------------------------------------------------------------ the common epilogue
 //
-// When everything but the bias is bf16 in rows of whole 32-byte units, 32 columns of a row
-// are 64 bytes of each operand.  With two epilogue warps per scheduler, the epilogue's pace
-// is its number of instructions times their latency, so this path has no choices inside:
-// addresses are carried per row, and the inputs are fetched a step ahead (16 words each).
+// When everything but the bias is bf16 in rows of whole 32-byte units, NC = 16 or 32 columns
+// of a row are one or two 32-byte accesses of each operand.  The epilogue's pace is its
+// number of instructions times their latency over the few warps that run it, so this path
+// has no choices inside: addresses are carried per row, and the inputs are fetched a step
+// ahead.
+template <int NC>
 struct EpiRow {
+  static constexpr int W = NC / 2;  // 32-bit words of NC bf16 values
   const uint8_t* slope;
   const uint8_t* add;
   uint8_t* preact;
   uint8_t* out;
-  uint32_t slope_w[16], add_w[16];
+  uint32_t slope_w[W], add_w[W];
 
   __device__ __forceinline__ void start(const Epilogue& e, int64_t m, int64_t n) {
     slope = e.slope.p == nullptr ? nullptr : static_cast<const uint8_t*>(e.slope.p) + 2 * (m * e.slope.ld + n);
@@ -155,12 +143,18 @@ struct EpiRow {
     out = static_cast<uint8_t*>(e.out.p) + 2 * (m * e.out.ld + n);
   }
 
-  static __device__ __forceinline__ void words(const uint8_t* p, uint32_t (&w)[16]) {
-    uint4 a, b, c, d;
-    ld_global_v8(p, a, b);
-    ld_global_v8(p + 32, c, d);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    w[8] = c.x, w[9] = c.y, w[10] = c.z, w[11] = c.w, w[12] = d.x, w[13] = d.y, w[14] = d.z, w[15] = d.w;
+  static __device__ __forceinline__ void words(const uint8_t* p, uint32_t (&w)[W]) {
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) {
+      uint4 a, b;
+      ld_global_v8(p + 32 * i, a, b);
+      w[8 * i] = a.x, w[8 * i + 1] = a.y, w[8 * i + 2] = a.z, w[8 * i + 3] = a.w;
+      w[8 * i + 4] = b.x, w[8 * i + 5] = b.y, w[8 * i + 6] = b.z, w[8 * i + 7] = b.w;
+    }
+  }
+
+  static __device__ __forceinline__ F2 value(uint32_t w) {
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
 
   __device__ __forceinline__ void fetch(int col) {
@@ -168,32 +162,33 @@ struct EpiRow {
     if (add != nullptr) words(add + 2 * col, add_w);
   }
 
-  static __device__ __forceinline__ void store(uint8_t* p, const F2 (&v)[16]) {
-    uint32_t w[16];
+  static __device__ __forceinline__ void store(uint8_t* p, const F2 (&v)[W]) {
+    uint32_t w[W];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < W; ++j) {
       const float2 f = split(v[j]);
       const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
       w[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    st_global_v8(p, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
-    st_global_v8(p + 32, make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i)
+      st_global_v8(p + 32 * i, make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]),
+                   make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]));
   }
 
-  // Columns [col, col + 32) of the row (from column n of the output), from the sums in v;
-  // `more`: the next 32 follow.
-  __device__ __forceinline__ void finish(const Epilogue& e, int64_t n, int col, bool more, F2 (&v)[16]) {
+  // Columns [col, col + NC) of the row (from column n of the output), from the sums in v;
+  // `more`: the next NC follow.
+  __device__ __forceinline__ void finish(const Epilogue& e, int64_t n, int col, bool more, F2 (&v)[W]) {
     if (e.bias.p != nullptr) {
       if (e.bias.bf16) {
-        uint32_t w[16];
+        uint32_t w[W];
         words(static_cast<const uint8_t*>(e.bias.p) + 2 * n, w);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          v[j] = add2(v[j], pair(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)));
+        for (int j = 0; j < W; ++j) v[j] = add2(v[j], value(w[j]));
       } else {
         const float* b = static_cast<const float*>(e.bias.p) + n;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < W / 4; ++j) {
           uint4 x, y;
           ld_global_v8(b + 8 * j, x, y);
           v[4 * j] = add2(v[4 * j], pair(__uint_as_float(x.x), __uint_as_float(x.y)));
@@ -204,38 +199,18 @@ struct EpiRow {
       }
     }
     if (preact != nullptr) store(preact + 2 * col, v);
-    if (e.act != MUON_ACT_NONE) {
-      float x[32];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 f = split(v[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
-      }
-      apply_act<32>(e.act, x);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = pair(x[2 * j], x[2 * j + 1]);
-    }
+    apply_act<W>(e.act, v);
     if (slope != nullptr) {
-      float t[32], x[32];
+      F2 t[W];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 f = split(v[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
-        t[2 * j] = __uint_as_float(slope_w[j] << 16);
-        t[2 * j + 1] = __uint_as_float(slope_w[j] & 0xFFFF0000u);
-      }
-      apply_slope<32>(e.slope_act, t, x);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = pair(x[2 * j], x[2 * j + 1]);
+      for (int j = 0; j < W; ++j) t[j] = value(slope_w[j]);
+      apply_slope<W>(e.slope_act, t, v);
     }
     if (add != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        v[j] = add2(v[j], pair(__uint_as_float(add_w[j] << 16), __uint_as_float(add_w[j] & 0xFFFF0000u)));
+      for (int j = 0; j < W; ++j) v[j] = add2(v[j], value(add_w[j]));
     }
-    if (more) fetch(col + 32);
+    if (more) fetch(col + NC);
     store(out + 2 * col, v);
   }
 };
@@ -248,66 +223,75 @@ __device__ __forceinline__ void prefetch_row(const EpiView& v, int64_t m, int64_
   for (int c = 0; c < cols; c += step) prefetch_l2(p + c * (v.bf16 ? 2 : 4));
 }
 
-// Row m, columns [n, n + NC) (n a multiple of 8) without a fetch ahead: the join kernel's.
+// Row m, columns [n, n + NC) of the output (n a multiple of 8), whatever its operands are.
 template <int NC>
-__device__ __forceinline__ void finish_segment(const Epilogue& e, int64_t m, int64_t n, float (&v)[NC]) {
+__device__ __forceinline__ void finish_segment(const Epilogue& e, int64_t m, int64_t n, F2 (&v)[NC / 2]) {
   const int64_t left = e.cols - n;
   if (m >= e.rows || left <= 0) return;
   const int valid = left < NC ? static_cast<int>(left) : NC;
-  float t[NC];
+  F2 t[NC / 2];
   if (e.bias.p != nullptr) {
-    load_segment<NC>(e.bias, n, valid, t);
+    load_pairs<NC>(e.bias, n, valid, t);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] += t[j];
+    for (int j = 0; j < NC / 2; ++j) v[j] = add2(v[j], t[j]);
   }
-  if (e.preact.p != nullptr) store_segment<NC>(e.preact, m * e.preact.ld + n, valid, v);
-  apply_act<NC>(e.act, v);
+  if (e.preact.p != nullptr) store_pairs<NC>(e.preact, m * e.preact.ld + n, valid, v);
+  apply_act<NC / 2>(e.act, v);
   if (e.slope.p != nullptr) {
-    load_segment<NC>(e.slope, m * e.slope.ld + n, valid, t);
-    apply_slope<NC>(e.slope_act, t, v);
+    load_pairs<NC>(e.slope, m * e.slope.ld + n, valid, t);
+    apply_slope<NC / 2>(e.slope_act, t, v);
   }
   if (e.add.p != nullptr) {
-    load_segment<NC>(e.add, m * e.add.ld + n, valid, t);
+    load_pairs<NC>(e.add, m * e.add.ld + n, valid, t);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] += t[j];
+    for (int j = 0; j < NC / 2; ++j) v[j] = add2(v[j], t[j]);
   }
-  store_segment<NC>(e.out, m * e.out.ld + n, valid, v);
+  store_pairs<NC>(e.out, m * e.out.ld + n, valid, v);
 }
 
 // Column n of rows [m, m + NC): neighbouring threads hold neighbouring columns.
 template <int NC>
-__device__ __forceinline__ void finish_column(const Epilogue& e, int64_t m, int64_t n, float (&v)[NC]) {
-  if (n >= e.cols) return;
+__device__ __forceinline__ void load_column(const EpiView& v, int64_t m, int64_t n, int valid, F2 (&x)[NC / 2]) {
+  float e[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) e[j] = j < valid ? load_elem(v.p, (m + j) * v.ld + n, v.bf16) : 0.f;
+#pragma unroll
+  for (int j = 0; j < NC / 2; ++j) x[j] = pair(e[2 * j], e[2 * j + 1]);
+}
+
+template <int NC>
+__device__ __forceinline__ void store_column(const EpiView& v, int64_t m, int64_t n, int valid,
+                                             const F2 (&x)[NC / 2]) {
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const float2 f = split(x[j / 2]);
+    if (j < valid) store_elem(v.p, (m + j) * v.ld + n, v.bf16, (j & 1) ? f.y : f.x);
+  }
+}
+
+template <int NC>
+__device__ __forceinline__ void finish_column(const Epilogue& e, int64_t m, int64_t n, F2 (&v)[NC / 2]) {
   const int64_t left = e.rows - m;
+  if (n >= e.cols || left <= 0) return;
   const int valid = left < NC ? static_cast<int>(left) : NC;
+  F2 t[NC / 2];
   if (e.bias.p != nullptr) {
-    const float b = load_elem(e.bias.p, n, e.bias.bf16);
+    const F2 b = pair(load_elem(e.bias.p, n, e.bias.bf16));
 #pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] += b;
+    for (int j = 0; j < NC / 2; ++j) v[j] = add2(v[j], b);
   }
-  if (e.preact.p != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NC; ++j)
-      if (j < valid) store_elem(e.preact.p, (m + j) * e.preact.ld + n, e.preact.bf16, v[j]);
-  }
-  apply_act<NC>(e.act, v);
-  float t[NC];
+  if (e.preact.p != nullptr) store_column<NC>(e.preact, m, n, valid, v);
+  apply_act<NC / 2>(e.act, v);
   if (e.slope.p != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NC; ++j)
-      t[j] = j < valid ? load_elem(e.slope.p, (m + j) * e.slope.ld + n, e.slope.bf16) : 0.f;
-    apply_slope<NC>(e.slope_act, t, v);
+    load_column<NC>(e.slope, m, n, valid, t);
+    apply_slope<NC / 2>(e.slope_act, t, v);
   }
   if (e.add.p != nullptr) {
+    load_column<NC>(e.add, m, n, valid, t);
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
-      t[j] = j < valid ? load_elem(e.add.p, (m + j) * e.add.ld + n, e.add.bf16) : 0.f;
-#pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] += t[j];
+    for (int j = 0; j < NC / 2; ++j) v[j] = add2(v[j], t[j]);
   }
-#pragma unroll
-  for (int j = 0; j < NC; ++j)
-    if (j < valid) store_elem(e.out.p, (m + j) * e.out.ld + n, e.out.bf16, v[j]);
+  store_column<NC>(e.out, m, n, valid, v);
 }
 
 }  // namespace muon

@@ -20,72 +20,6 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, int bf16, float v
     static_cast<float*>(p)[i] = v;
 }
 
-__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
-
-// Phi(-|z|) and exp(-z^2 / 2), for the exact GELU.  With x = |z| / sqrt 2 and t = 1 / (1 + 0.3 x),
-// erfc(x) exp(x^2) / t is smooth on (0, 1]; the polynomial is its minimax fit (relative error)
-// of degree 8 for x <= 10, found by iteratively reweighted least squares on Chebyshev points:
-// 2e-8 in exact arithmetic, 5e-7 as evaluated in fp32, in the far tail too.
-__device__ __forceinline__ float normal_tail(float z, float& bell) {
-  bell = __expf(-0.5f * z * z);
-  const float t = __fdividef(1.f, fmaf(0.3f * 0.70710678118654752f, fabsf(z), 1.f));
-  float q = -0.06476138532161713f;
-  q = fmaf(q, t, 0.24278128147125244f);
-  q = fmaf(q, t, -0.2561383843421936f);
-  q = fmaf(q, t, 0.27385929226875305f);
-  q = fmaf(q, t, -0.04732486978173256f);
-  q = fmaf(q, t, 0.1074628233909607f);
-  q = fmaf(q, t, 0.07416963577270508f);
-  q = fmaf(q, t, 0.08535760641098022f);
-  q = fmaf(q, t, 0.0845940038561821f);
-  return q * t * bell;
-}
-
-// act(z) in fp32.  The tanh form is z sigmoid(2 u): (1 + tanh u) / 2 = sigmoid(2 u), which
-// keeps its relative accuracy where 1 + tanh u cancels.  Comparisons are written so that a
-// NaN comes out as a NaN.
-__device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case MUON_ACT_RELU: return z < 0.f ? 0.f : z;
-    case MUON_ACT_RELU2: {
-      const float r = z < 0.f ? 0.f : z;
-      return r * r;
-    }
-    case MUON_ACT_GELU: {
-      float bell;
-      const float tail = normal_tail(z, bell);
-      return z * (z < 0.f ? tail : 1.f - tail);
-    }
-    case MUON_ACT_GELU_TANH: return z * sigmoid(1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.f));
-    case MUON_ACT_SILU: return z * sigmoid(z);
-    default: return z;
-  }
-}
-
-// act'(z) in fp32.  The second terms vanish long before |z| = 64; clamping z there keeps
-// infinity times zero out of them.
-__device__ __forceinline__ float act_slope(int act, float z) {
-  const float c = fminf(fmaxf(z, -64.f), 64.f);
-  switch (act) {
-    case MUON_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case MUON_ACT_RELU2: return z < 0.f ? 0.f : 2.f * z;
-    case MUON_ACT_GELU: {
-      float bell;
-      const float tail = normal_tail(z, bell);
-      return fmaf(c * 0.39894228040143268f, bell, z < 0.f ? tail : 1.f - tail);
-    }
-    case MUON_ACT_GELU_TANH: {
-      const float p = sigmoid(1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.f));
-      return fmaf(c * p * (1.f - p), 1.5957691216057308f * fmaf(0.134145f * c, c, 1.f), p);
-    }
-    case MUON_ACT_SILU: {
-      const float p = sigmoid(z);
-      return p * fmaf(c, 1.f - p, 1.f);
-    }
-    default: return 1.f;
-  }
-}
-
 // Two fp32 values in one register pair: sm_100 adds, multiplies and fuses both in one
 // instruction.
 using F2 = unsigned long long;
@@ -115,6 +49,161 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+// 2^x and 1 / x by the special function unit (a unit or two of the last place; 1 / inf = 0).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// z clamped to [-128, 128], a NaN kept: there every derivative is at its limit in fp32, so that
+// infinity times zero does not come up.
+__device__ __forceinline__ float clamp128(float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(-128.f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(128.f));
+  return r;
+}
+
+// 1 / (1 + 2^t) for both of t.
+__device__ __forceinline__ F2 sigmoid2(F2 t) {
+  const float2 v = split(t);
+  const F2 d = add2(pair(fast_exp2(v.x), fast_exp2(v.y)), pair(1.f));
+  const float2 w = split(d);
+  return pair(fast_rcp(w.x), fast_rcp(w.y));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+// The exponent of 2 in (1 + tanh u) / 2 = sigmoid(2 u) = 1 / (1 + 2^t), for
+// 2 u = kTanhScale (z + 0.044715 z^3); this form keeps its relative accuracy where
+// 1 + tanh u cancels.
+__device__ __forceinline__ F2 tanh_exponent(F2 z, F2 zz) {
+  return mul2(z, fma2(zz, pair(-kLog2e * kTanhScale * 0.044715f), pair(-kLog2e * kTanhScale)));
+}
+
+// Phi(-|z|) and exp(-z^2 / 2), for the exact GELU.  With x = |z| / sqrt 2 and t = 1 / (1 + 0.3 x),
+// erfc(x) exp(x^2) / t is smooth on (0, 1]; the polynomial is its minimax fit (relative error)
+// of degree 8 for x <= 10, found by iteratively reweighted least squares on Chebyshev points:
+// 2e-8 in exact arithmetic, 5e-7 as evaluated in fp32, in the far tail too.
+__device__ __forceinline__ F2 normal_tail2(F2 z, F2& bell) {
+  const float2 e = split(mul2(mul2(z, z), pair(-0.5f * kLog2e)));
+  bell = pair(fast_exp2(e.x), fast_exp2(e.y));
+  const float2 v = split(z);
+  const float2 d = split(fma2(pair(fabsf(v.x), fabsf(v.y)), pair(0.3f * 0.70710678118654752f), pair(1.f)));
+  const F2 t = pair(fast_rcp(d.x), fast_rcp(d.y));
+  F2 q = pair(-0.06476138532161713f);
+  q = fma2(q, t, pair(0.24278128147125244f));
+  q = fma2(q, t, pair(-0.2561383843421936f));
+  q = fma2(q, t, pair(0.27385929226875305f));
+  q = fma2(q, t, pair(-0.04732486978173256f));
+  q = fma2(q, t, pair(0.1074628233909607f));
+  q = fma2(q, t, pair(0.07416963577270508f));
+  q = fma2(q, t, pair(0.08535760641098022f));
+  q = fma2(q, t, pair(0.0845940038561821f));
+  return mul2(mul2(q, t), bell);
+}
+
+// Phi(z) from Phi(-|z|).
+__device__ __forceinline__ F2 normal_cdf2(F2 z, F2 tail) {
+  const float2 v = split(z), w = split(tail);
+  return pair(v.x < 0.f ? w.x : 1.f - w.x, v.y < 0.f ? w.y : 1.f - w.y);
+}
+
+__device__ __forceinline__ F2 relu2_of(F2 z) {  // max(z, 0); a NaN stays one
+  const float2 v = split(z);
+  return pair(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);
+}
+
+// act(z) in fp32, two at a time: epilogues are paced by their instructions.
+template <int ACT>
+__device__ __forceinline__ F2 act_value2(F2 z) {
+  if constexpr (ACT == MUON_ACT_RELU) {
+    return relu2_of(z);
+  } else if constexpr (ACT == MUON_ACT_RELU2) {
+    const F2 r = relu2_of(z);
+    return mul2(r, r);
+  } else if constexpr (ACT == MUON_ACT_GELU) {
+    F2 bell;
+    const F2 tail = normal_tail2(z, bell);
+    return mul2(z, normal_cdf2(z, tail));
+  } else if constexpr (ACT == MUON_ACT_GELU_TANH) {
+    return mul2(z, sigmoid2(tanh_exponent(z, mul2(z, z))));
+  } else {
+    static_assert(ACT == MUON_ACT_SILU, "an activation");
+    return mul2(z, sigmoid2(mul2(z, pair(-kLog2e))));
+  }
+}
+
+// act'(z) in fp32.
+template <int ACT>
+__device__ __forceinline__ F2 act_slope2(F2 z) {
+  if constexpr (ACT == MUON_ACT_RELU) {
+    const float2 v = split(z);
+    return pair(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
+  } else if constexpr (ACT == MUON_ACT_RELU2) {
+    return mul2(relu2_of(z), pair(2.f));
+  } else {
+    const float2 v = split(z);
+    z = pair(clamp128(v.x), clamp128(v.y));
+    if constexpr (ACT == MUON_ACT_GELU) {
+      F2 bell;
+      const F2 tail = normal_tail2(z, bell);
+      return fma2(mul2(z, pair(0.39894228040143268f)), bell, normal_cdf2(z, tail));
+    } else if constexpr (ACT == MUON_ACT_GELU_TANH) {
+      // p + z p (1 - p) kTanhScale (1 + 3 0.044715 z^2)
+      const F2 zz = mul2(z, z), p = sigmoid2(tanh_exponent(z, zz));
+      const F2 g = mul2(z, fma2(zz, pair(kTanhScale * 0.134145f), pair(kTanhScale)));
+      return mul2(p, fma2(g, fma2(p, pair(-1.f), pair(1.f)), pair(1.f)));
+    } else {
+      static_assert(ACT == MUON_ACT_SILU, "an activation");
+      const F2 p = sigmoid2(mul2(z, pair(-kLog2e)));
+      return mul2(p, fma2(z, fma2(p, pair(-1.f), pair(1.f)), pair(1.f)));
+    }
+  }
+}
+
+// v = act(v) and v *= act'(t), the choice made once for N pairs.
+template <int N>
+__device__ __forceinline__ void apply_act(int act, F2 (&v)[N]) {
+#define MUON_EACH(A)                                                        \
+  case A:                                                                   \
+    _Pragma("unroll") for (int j = 0; j < N; ++j) v[j] = act_value2<A>(v[j]); \
+    break
+  switch (act) {
+    MUON_EACH(MUON_ACT_RELU);
+    MUON_EACH(MUON_ACT_RELU2);
+    MUON_EACH(MUON_ACT_GELU);
+    MUON_EACH(MUON_ACT_GELU_TANH);
+    MUON_EACH(MUON_ACT_SILU);
+    default: break;
+  }
+#undef MUON_EACH
+}
+
+template <int N>
+__device__ __forceinline__ void apply_slope(int act, const F2 (&t)[N], F2 (&v)[N]) {
+#define MUON_EACH(A)                                                                        \
+  case A:                                                                                   \
+    _Pragma("unroll") for (int j = 0; j < N; ++j) v[j] = mul2(v[j], act_slope2<A>(t[j])); \
+    break
+  switch (act) {
+    MUON_EACH(MUON_ACT_RELU);
+    MUON_EACH(MUON_ACT_RELU2);
+    MUON_EACH(MUON_ACT_GELU);
+    MUON_EACH(MUON_ACT_GELU_TANH);
+    MUON_EACH(MUON_ACT_SILU);
+    default: break;
+  }
+#undef MUON_EACH
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -95,11 +95,11 @@ __global__ void __launch_bounds__(256) muon_activation_backward_kernel(const __g
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int64_t r = i / groups, c = (i - r * groups) * 8;
     const int valid = p.cols - c < 8 ? static_cast<int>(p.cols - c) : 8;
-    float g[8], z[8];
-    load_segment<8>(p.dy, r * p.dy.ld + c, valid, g);
-    load_segment<8>(p.z, r * p.z.ld + c, valid, z);
-    apply_slope<8>(p.act, z, g);
-    store_segment<8>(p.dz, r * p.dz.ld + c, valid, g);
+    F2 g[4], z[4];
+    load_pairs<8>(p.dy, r * p.dy.ld + c, valid, g);
+    load_pairs<8>(p.z, r * p.z.ld + c, valid, z);
+    apply_slope<4>(p.act, z, g);
+    store_pairs<8>(p.dz, r * p.dz.ld + c, valid, g);
   }
 }
 
