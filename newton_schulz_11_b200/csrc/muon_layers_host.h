@@ -114,7 +114,7 @@ unsigned long long layers_wait_ns();
 // Reads (or clears) the status word of the norm kernels, queued on `s`.
 cudaError_t norm_status(int32_t (&out)[2], bool clear, cudaStream_t s);
 
-inline muon_status_t launched() { return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA; }
+inline muon_status_t queued(cudaError_t e) { return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA; }
 
 constexpr int64_t kMaxSide = int64_t(1) << 24;  // columns, features (as for muon_matrix_t)
 constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens

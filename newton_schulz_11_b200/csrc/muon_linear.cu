@@ -19,88 +19,30 @@
 
 namespace muon {
 
-struct ColumnSumParams {
-  const void* dy;
-  float* db;
-  float* partial;  // [slices][ld_partial]
-  int64_t rows, ld, ld_partial;
-  int32_t cols, bf16, vec, accumulate, slices;
-};
-
-// Sums of columns over the rows: block (b, s) takes 256 columns, 8 a thread, and every
-// slices-th group of 8 rows.
-__global__ void __launch_bounds__(256) muon_column_sum_kernel(const __grid_constant__ ColumnSumParams p) {
-  __shared__ float red[8][256];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 256 + lane * 8;
-  const EpiView src{const_cast<void*>(p.dy), p.ld, p.bf16, p.vec};
-  float s[8] = {};
-  if (c < p.cols) {
-#pragma unroll 4
-    for (int64_t r = blockIdx.y * 8 + w; r < p.rows; r += int64_t(8) * gridDim.y) {
-      float x[8];
-      load_segment<8>(src, r * p.ld + c, p.cols - c, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += x[j];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) red[w][lane * 8 + j] = s[j];
-  __syncthreads();
-  const int o = blockIdx.x * 256 + threadIdx.x;
-  if (o < p.cols) {
-    float t = red[0][threadIdx.x];
-    for (int k = 1; k < 8; ++k) t += red[k][threadIdx.x];
-    if (p.slices == 1)
-      p.db[o] = p.accumulate ? p.db[o] + t : t;
-    else
-      p.partial[blockIdx.y * p.ld_partial + o] = t;
-  }
-}
-
-// 32 columns per block, 8 warps over the slices.
-__global__ void __launch_bounds__(256) muon_column_join_kernel(const __grid_constant__ ColumnSumParams p) {
-  __shared__ float red[8][32];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float t = 0.f;
-  if (c < p.cols) {
-#pragma unroll 4
-    for (int s = w; s < p.slices; s += 8) t += p.partial[s * p.ld_partial + c];
-  }
-  red[w][lane] = t;
-  __syncthreads();
-  if (w == 0 && c < p.cols) {
-    for (int k = 1; k < 8; ++k) t += red[k][lane];
-    p.db[c] = p.accumulate ? p.db[c] + t : t;
-  }
-}
-
 struct ActGradParams {
   EpiView dy, z, dz;
-  int64_t rows, cols;
-  int32_t act;
+  Sweep sweep;
+  int32_t cols, act;
 };
 
-// Eight columns of a row per thread.
-__global__ void __launch_bounds__(256) muon_activation_backward_kernel(const __grid_constant__ ActGradParams p) {
-  griddep_launch_dependents();
+// Eight columns of a row per thread and step.
+__global__ void __launch_bounds__(256, 6) muon_activation_backward_kernel(const __grid_constant__ ActGradParams p) {
   griddep_wait();
-  const int64_t groups = (p.cols + 7) / 8;
-  const int64_t total = groups * p.rows;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t r = i / groups, c = (i - r * groups) * 8;
-    const int valid = p.cols - c < 8 ? static_cast<int>(p.cols - c) : 8;
-    F2 g[4], z[4];
-    load_pairs<8>(p.dy, r * p.dy.ld + c, valid, g);
-    load_pairs<8>(p.z, r * p.z.ld + c, valid, z);
-    apply_slope<4>(p.act, z, g);
-    store_pairs<8>(p.dz, r * p.dz.ld + c, valid, g);
-  }
+  griddep_launch_dependents();
+  const Sweep& s = p.sweep;
+  const int along = 1 << s.shift, deep = 256 >> s.shift;
+  const int rb = blockIdx.x / s.col_blocks, cb = blockIdx.x - rb * s.col_blocks;
+  const int g0 = (cb << s.shift) + (threadIdx.x & (along - 1));
+  for (int64_t r = static_cast<int64_t>(rb) * deep + (threadIdx.x >> s.shift); r < s.rows;
+       r += static_cast<int64_t>(s.row_blocks) * deep)
+    for (int gr = g0; gr < s.groups; gr += s.col_blocks << s.shift) {
+      const int c = gr * 8, valid = p.cols - c;
+      F2 g[4], z[4];
+      load_pairs<8>(p.dy, r * p.dy.ld + c, valid, g);
+      load_pairs<8>(p.z, r * p.z.ld + c, valid, z);
+      apply_slope<4>(p.act, z, g);
+      store_pairs<8>(p.dz, r * p.dz.ld + c, valid, g);
+    }
 }
 
 }  // namespace muon
@@ -222,21 +164,19 @@ Plan make_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool may_fli
   return e.plan;
 }
 
-muon_status_t pack(const Operand& o, uint8_t* ws, cudaStream_t s) {
-  if (o.direct || o.rows == 0) return MUON_OK;
-  const EpiView src = epi_view(*o.v, o.rows, o.cols);
-  PackParams p{};
-  p.src = src.p;
-  p.dst = reinterpret_cast<__nv_bfloat16*>(ws + o.offset);
-  p.rows = o.rows;
-  p.ld_src = src.ld;
-  p.ld_dst = o.ld_packed;
-  p.term_stride = static_cast<int64_t>(o.term_bytes() / 2);
-  p.cols = static_cast<int32_t>(o.cols);
-  p.src_bf16 = src.bf16;
-  p.terms = o.terms;
-  p.vec = src.vec;
-  return launch_pack(p, kSms, s) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+// Adds the layout of `o` to the call's first launch, unless it is read in place.
+void add_pack(PrepareParams* p, const Operand& o, uint8_t* ws) {
+  if (o.direct || o.rows == 0) return;
+  PackTask& t = p->pack[p->packs];
+  t.src = epi_view(*o.v, o.rows, o.cols);
+  t.dst = reinterpret_cast<__nv_bfloat16*>(ws + o.offset);
+  t.ld_dst = o.ld_packed;
+  t.term_stride = static_cast<int64_t>(o.term_bytes() / 2);
+  t.cols = static_cast<int32_t>(o.cols);
+  t.terms = o.terms;
+  t.sweep = make_sweep(o.rows, o.ld_packed / 8, 8 * kSms);
+  p->begin[p->packs + 1] = p->begin[p->packs] + sweep_blocks(t.sweep);
+  ++p->packs;
 }
 
 // `side_rows`: how many of the operand's side a box of a K-major operand covers.
@@ -255,9 +195,10 @@ bool plain_epilogue(const Epilogue& e) {
   return e.bias.p == nullptr || e.bias.vec == 2;
 }
 
-// a: the operand on the output's row side; b: on its column side.  mn: contiguous along the side.
+// a: the operand on the output's row side; b: on its column side.  mn: contiguous along the
+// side.  A split reduction leaves its end to `finish`.
 muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const Epilogue& e,
-                          uint8_t* ws, size_t partial_at, cudaStream_t s) {
+                          uint8_t* ws, size_t partial_at, bool beside, FinishParams* finish, cudaStream_t s) {
   static const uint8_t both_a[kMaxSegments] = {0, 2, 1, 0, 1, 0}, both_b[kMaxSegments] = {2, 0, 1, 1, 0, 0};
   const bool flip = pl.tile >= kFlip32;
   const Operand &am = flip ? b : a, &bm = flip ? a : b;
@@ -280,23 +221,23 @@ muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Ope
     p.seg_a[g] = static_cast<uint8_t>(am.terms == 1 ? 0 : bm.terms == 1 ? pl.nseg - 1 - g : both_a[g]);
     p.seg_b[g] = static_cast<uint8_t>(bm.terms == 1 ? 0 : am.terms == 1 ? pl.nseg - 1 - g : both_b[g]);
   }
+  p.beside = beside ? 1 : 0;
   p.timeout_ns = layers_wait_ns();
   if (pl.splits > 1) {
     p.partial = reinterpret_cast<float*>(ws + partial_at);
     p.ld_partial = pl.ld_partial;
     p.split_stride = e.rows * pl.ld_partial;
-  }
-  if (launch_product(pl.tile, p, kSms, s) != cudaSuccess) return MUON_ERR_CUDA;
-  if (pl.splits > 1) {
-    JoinParams j{};
+    JoinTask& j = finish->join[finish->joins];
     j.e = e;
     j.partial = p.partial;
     j.ld_partial = p.ld_partial;
     j.split_stride = p.split_stride;
     j.splits = p.splits;
-    if (launch_join(j, kSms, s) != cudaSuccess) return MUON_ERR_CUDA;
+    j.sweep = make_sweep(e.rows, ceil_div(e.cols, 8), 8 * kSms);
+    finish->begin[finish->joins + 1] = finish->begin[finish->joins] + sweep_blocks(j.sweep);
+    ++finish->joins;
   }
-  return MUON_OK;
+  return queued(launch_product(pl.tile, p, kSms, s));
 }
 
 bool wants_sum(const muon_view_t& out) { return out.data != nullptr && out.dtype == MUON_F32; }
@@ -325,7 +266,7 @@ struct LinearGradPlan {
   Operand dy, x, w;
   Plan dx, dw;
   int64_t slices = 0;
-  size_t partial_at = 0, db_at = 0, bytes = 0;
+  size_t dx_at = 0, dw_at = 0, db_at = 0, bytes = 0;
 };
 
 LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
@@ -334,21 +275,20 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
   const bool dx = d->dx.data != nullptr, dw = d->dw.data != nullptr;
   pl.dy = Operand(d->dy, d->rows, d->out);
   if (dx || dw) pl.dy.place(&pl.bytes);
-  size_t partial = 0;
   if (dx) {
     pl.w = Operand(d->w, d->out, d->in);
     pl.w.place(&pl.bytes);
     pl.dx = make_plan(d->rows, d->in, d->out, segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), true);
-    partial = pl.dx.partial_bytes;
+    pl.dx_at = pl.bytes;
+    pl.bytes += pl.dx.partial_bytes;
   }
   if (dw) {
     pl.x = Operand(d->x, d->rows, d->in);
     pl.x.place(&pl.bytes);
     pl.dw = make_plan(d->out, d->in, d->rows, segments(pl.dy.terms, pl.x.terms), true, false);
-    partial = std::max(partial, pl.dw.partial_bytes);  // the products run one after the other
+    pl.dw_at = pl.bytes;
+    pl.bytes += pl.dw.partial_bytes;
   }
-  pl.partial_at = pl.bytes;
-  pl.bytes += partial;
   if (d->db != nullptr) {
     pl.slices = std::max<int64_t>(1, std::min(d->rows / 128, 4 * kSms / ceil_div(d->out, 256)));
     pl.db_at = pl.bytes;
@@ -363,20 +303,6 @@ muon_status_t take_workspace(Operands* ops, void* ws, size_t have, size_t need) 
   if (!aligned_bytes(ws, 256)) return MUON_ERR_ALIGNMENT;
   ops->add_bytes(ws, need);
   return MUON_OK;
-}
-
-template <class K, class P>
-muon_status_t launch_after(K kernel, const P& p, dim3 grid, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 // The checks of a descriptor without its workspace, so that sizing a call checks it too.
@@ -434,7 +360,14 @@ muon_status_t muon_linear(const muon_linear_t* d, void* workspace, size_t worksp
   if (d->rows == 0) return MUON_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((st = pack(pl.x, ws, s)) != MUON_OK || (st = pack(pl.w, ws, s)) != MUON_OK) return st;
+  PrepareParams before{};
+  FinishParams after{};
+  add_pack(&before, pl.x, ws);
+  add_pack(&before, pl.w, ws);
+  if (before.packs > 0) {
+    before.begin[before.packs + 1] = before.begin[before.packs];
+    if ((st = queued(launch_prepare(before, s))) != MUON_OK) return st;
+  }
   Epilogue e{};
   e.rows = d->rows;
   e.cols = d->out;
@@ -443,7 +376,10 @@ muon_status_t muon_linear(const muon_linear_t* d, void* workspace, size_t worksp
   e.add = epi_view(d->residual, d->rows, d->out);
   e.out = epi_view(d->y, d->rows, d->out);
   e.act = d->act;
-  return run_product(pl.z, pl.x, false, pl.w, false, e, ws, pl.partial_at, s);
+  st = run_product(pl.z, pl.x, false, pl.w, false, e, ws, pl.partial_at, false, &after, s);
+  if (st != MUON_OK || after.joins == 0) return st;
+  after.begin[after.joins + 1] = after.begin[after.joins];
+  return queued(launch_finish(after, s));
 }
 
 muon_status_t muon_linear_backward_workspace(const muon_linear_grad_t* d, size_t* bytes) {
@@ -477,10 +413,27 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     return MUON_OK;
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (dx || dw)
-    if ((st = pack(pl.dy, ws, s)) != MUON_OK) return st;
+  PrepareParams before{};
+  FinishParams after{};
+  if (dx || dw) add_pack(&before, pl.dy, ws);
+  if (dx) add_pack(&before, pl.w, ws);
+  if (dw) add_pack(&before, pl.x, ws);
+  before.begin[before.packs + 1] = before.begin[before.packs];
+  if (d->db != nullptr) {
+    ColumnSumTask& t = before.sum;
+    t.src = epi_view(d->dy, d->rows, d->out);
+    t.out = d->db;
+    t.partial = reinterpret_cast<float*>(ws + pl.db_at);
+    t.rows = d->rows;
+    t.cols = static_cast<int32_t>(d->out);
+    t.accumulate = d->accumulate;
+    t.slices = static_cast<int32_t>(pl.slices);
+    before.begin[before.packs + 1] += static_cast<int32_t>(ceil_div(d->out, 256) * pl.slices);
+    after.sum = t;
+  }
+  if (before.begin[before.packs + 1] > 0)
+    if ((st = queued(launch_prepare(before, s))) != MUON_OK) return st;
   if (dx) {
-    if ((st = pack(pl.w, ws, s)) != MUON_OK) return st;
     Epilogue e{};
     e.rows = d->rows;
     e.cols = d->in;
@@ -490,36 +443,20 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     }
     e.add = epi_view(d->skip, d->rows, d->in);
     e.out = epi_view(d->dx, d->rows, d->in);
-    if ((st = run_product(pl.dx, pl.dy, false, pl.w, true, e, ws, pl.partial_at, s)) != MUON_OK) return st;
+    st = run_product(pl.dx, pl.dy, false, pl.w, true, e, ws, pl.dx_at, false, &after, s);
+    if (st != MUON_OK) return st;
   }
   if (dw) {
-    if ((st = pack(pl.x, ws, s)) != MUON_OK) return st;
     Epilogue e{};
     e.rows = d->out;
     e.cols = d->in;
     e.out = epi_view(d->dw, d->out, d->in);
     if (d->accumulate) e.add = e.out;
-    if ((st = run_product(pl.dw, pl.dy, true, pl.x, true, e, ws, pl.partial_at, s)) != MUON_OK) return st;
+    if ((st = run_product(pl.dw, pl.dy, true, pl.x, true, e, ws, pl.dw_at, dx, &after, s)) != MUON_OK) return st;
   }
-  if (d->db != nullptr) {
-    const EpiView dy = epi_view(d->dy, d->rows, d->out);
-    ColumnSumParams c{};
-    c.dy = dy.p;
-    c.db = d->db;
-    c.partial = reinterpret_cast<float*>(ws + pl.db_at);
-    c.rows = d->rows;
-    c.ld = dy.ld;
-    c.ld_partial = d->out;
-    c.cols = static_cast<int32_t>(d->out);
-    c.bf16 = dy.bf16;
-    c.vec = dy.vec;
-    c.accumulate = d->accumulate;
-    c.slices = static_cast<int32_t>(pl.slices);
-    const unsigned blocks = static_cast<unsigned>(ceil_div(d->out, 256));
-    if ((st = launch_after(muon_column_sum_kernel, c, dim3(blocks, c.slices), s)) != MUON_OK) return st;
-    if (c.slices > 1) return launch_after(muon_column_join_kernel, c, dim3(static_cast<unsigned>(ceil_div(d->out, 32))), s);
-  }
-  return MUON_OK;
+  after.begin[after.joins + 1] = after.begin[after.joins];
+  if (pl.slices > 1) after.begin[after.joins + 1] += static_cast<int32_t>(ceil_div(d->out, 32));
+  return after.begin[after.joins + 1] > 0 ? queued(launch_finish(after, s)) : MUON_OK;
 }
 
 muon_status_t muon_activation_backward(const muon_activation_grad_t* d, void* stream) {
@@ -539,12 +476,12 @@ muon_status_t muon_activation_backward(const muon_activation_grad_t* d, void* st
   p.dy = epi_view(d->dy, d->rows, d->cols);
   p.z = epi_view(d->z, d->rows, d->cols);
   p.dz = epi_view(d->dz, d->rows, d->cols);
-  p.rows = d->rows;
-  p.cols = d->cols;
+  p.sweep = make_sweep(d->rows, ceil_div(d->cols, 8), 12 * kSms);
+  p.cols = static_cast<int32_t>(d->cols);
   p.act = d->act;
-  const int64_t blocks = std::min<int64_t>(ceil_div(d->rows * ceil_div(d->cols, 8), 256), int64_t(kSms) * 32);
-  return launch_after(muon_activation_backward_kernel, p, dim3(static_cast<unsigned>(blocks)),
-                      static_cast<cudaStream_t>(stream));
+  return queued(launch_dependent(muon_activation_backward_kernel, p,
+                                 dim3(static_cast<unsigned>(sweep_blocks(p.sweep))), 256,
+                                 static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(L::kThreads, L::kForward) muon_layer_norm_ring
     fence_mbar_init();
   }
   __syncthreads();
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const Watchdog wd{&abort_flag, g_norm_status, p.timeout_ns};
   const uint32_t bytes = static_cast<uint32_t>(p.cols) * (L::BF16 ? 2 : 4), slot = slot_bytes(bytes);
   const Ring ring{full[group], rows + static_cast<uint32_t>(group * p.stages) * slot, slot, p.stages, wd};
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(L::kThreads, L::kBackward) muon_layer_norm_bac
     fence_mbar_init();
   }
   __syncthreads();
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const Watchdog wd{&abort_flag, g_norm_status, p.timeout_ns};
   const uint32_t bytes = static_cast<uint32_t>(p.cols) * (L::BF16 ? 2 : 4);
   const uint32_t skip_bytes = p.skip.p == nullptr ? 0u : static_cast<uint32_t>(p.cols) * (p.skip.bf16 ? 2 : 4);
@@ -519,8 +519,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // One row per block, read three times (from L2 after the first).
 __global__ void __launch_bounds__(kWideThreads) muon_layer_norm_wide_kernel(const __grid_constant__ NormParams p) {
   __shared__ float red[33];
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const int64_t xo = r * p.x.ld, yo = r * p.y.ld;
     float s = 0.f;
@@ -548,8 +548,8 @@ __global__ void __launch_bounds__(kWideThreads) muon_layer_norm_wide_kernel(cons
 __global__ void __launch_bounds__(kWideThreads) muon_layer_norm_dx_wide_kernel(
     const __grid_constant__ NormGradParams p) {
   __shared__ float red[33];
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const float mean = p.mean[r], rstd = p.rstd[r];
     float sq = 0.f, sqh = 0.f;
@@ -576,8 +576,8 @@ __global__ void __launch_bounds__(kWideThreads) muon_layer_norm_dx_wide_kernel(
 // of 8 rows.
 __global__ void __launch_bounds__(256) muon_layer_norm_columns_kernel(const __grid_constant__ NormGradParams p) {
   __shared__ float sg[8][33], sb[8][33];
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float dg = 0.f, db = 0.f;
@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(256) muon_layer_norm_columns_kernel(const __gr
 // Adds the slices' partial sums: 32 columns per block, 16 warps over the slices.
 __global__ void __launch_bounds__(512) muon_layer_norm_join_kernel(const __grid_constant__ NormGradParams p) {
   __shared__ float sum[16][2][32];
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float dg = 0.f, db = 0.f;
@@ -656,21 +656,6 @@ bool whole_groups(int64_t cols, std::initializer_list<const EpiView*> views) {
   return true;
 }
 
-template <class K, class P>
-muon_status_t launch_after(K kernel, const P& p, dim3 grid, int threads, cudaStream_t s, int smem = 0) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
-}
-
 // Blocks of a row kernel: what the SMs can hold at once, `per_sm` blocks each.
 int64_t row_blocks(int64_t rows, int groups, int per_sm) {
   return std::max<int64_t>(1, std::min<int64_t>(ceil_div(rows, groups), int64_t(kSms) * per_sm));
@@ -716,7 +701,7 @@ muon_status_t launch_rows(const P& p, int64_t blocks, int threads, int smem, cud
       return MUON_ERR_CUDA;
     configured_device = dev;
   }
-  return launch_after(Kernel, p, dim3(static_cast<unsigned>(blocks)), threads, s, smem);
+  return queued(launch_dependent(Kernel, p, dim3(static_cast<unsigned>(blocks)), threads, s, smem));
 }
 
 template <int T, int N, bool BF16, bool VEC>
@@ -791,8 +776,8 @@ extern "C" muon_status_t muon_layer_norm(const muon_layer_norm_t* d, void* strea
   p.timeout_ns = layers_wait_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->cols > kWidest)
-    return launch_after(muon_layer_norm_wide_kernel, p, dim3(static_cast<unsigned>(row_blocks(d->rows, 1, 4))),
-                        kWideThreads, s);
+    return queued(launch_dependent(muon_layer_norm_wide_kernel, p,
+                                   dim3(static_cast<unsigned>(row_blocks(d->rows, 1, 4))), kWideThreads, s));
   const bool vec = whole_groups(d->cols, {&p.x, &p.y, &p.gain, &p.bias}), bf16 = p.x.bf16 != 0;
   return with_shape(d->cols, [&](auto t, auto n) {
     if (vec) return bf16 ? run_norm<t(), n(), true, true>(p, s) : run_norm<t(), n(), false, true>(p, s);
@@ -862,11 +847,12 @@ extern "C" muon_status_t muon_layer_norm_backward(const muon_layer_norm_grad_t* 
   p.slices = slices_for(d);
   if (d->cols > kWidest) {
     if (d->dx.data != nullptr)
-      st = launch_after(muon_layer_norm_dx_wide_kernel, p, dim3(static_cast<unsigned>(row_blocks(d->rows, 1, 4))),
-                        kWideThreads, s);
+      st = queued(launch_dependent(muon_layer_norm_dx_wide_kernel, p,
+                                   dim3(static_cast<unsigned>(row_blocks(d->rows, 1, 4))), kWideThreads, s));
     if (st == MUON_OK && grads)
-      st = launch_after(muon_layer_norm_columns_kernel, p,
-                        dim3(static_cast<unsigned>(ceil_div(d->cols, 32)), static_cast<unsigned>(p.slices)), 256, s);
+      st = queued(launch_dependent(
+          muon_layer_norm_columns_kernel, p,
+          dim3(static_cast<unsigned>(ceil_div(d->cols, 32)), static_cast<unsigned>(p.slices)), 256, s));
   } else {
     const bool vec = whole_groups(d->cols, {&p.x, &p.dy, &p.gain, &p.skip, &p.dx}), bf16 = p.x.bf16 != 0;
     st = with_shape(d->cols, [&](auto t, auto n) {
@@ -875,5 +861,6 @@ extern "C" muon_status_t muon_layer_norm_backward(const muon_layer_norm_grad_t* 
     });
   }
   if (st != MUON_OK || !grads) return st;
-  return launch_after(muon_layer_norm_join_kernel, p, dim3(static_cast<unsigned>(ceil_div(d->cols, 32))), 512, s);
+  return queued(launch_dependent(muon_layer_norm_join_kernel, p, dim3(static_cast<unsigned>(ceil_div(d->cols, 32))),
+                                 512, s));
 }

@@ -182,7 +182,6 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
   volatile uint32_t* peer_issued = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);  // leader CTA
   __shared__ uint64_t pdone;  // leader CTA: the peer's producer has finished
 
-  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
@@ -225,7 +224,12 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
   const Watchdog wd{abort_flag, g_layers_status, p.timeout_ns};
   // waits on the way out, for copies and MMAs in flight, end by themselves
   const unsigned long long tb = p.timeout_ns > 2000000000ull ? p.timeout_ns : 2000000000ull;
-  griddep_wait();  // everything read or written below may belong to the launch before
+  // Everything read or written below may belong to the launch before.  A product that runs
+  // beside the one before it (the two of a backward pass) depends on what came before that
+  // one only: its blocks start once all blocks of the other have passed this wait, so it
+  // need not wait here; it waits at its end, so that whatever follows finds both complete.
+  if (!p.beside) griddep_wait();
+  griddep_launch_dependents();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (each CTA)
@@ -469,6 +473,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
     }
   }
 
+  if (p.beside) griddep_wait();
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();  // nothing arrives on, or lands in, either CTA after this
@@ -481,86 +486,140 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
   }
 }
 
-// ------------------------------------------------------------------ joining split reductions
+// ------------------------------------------------------------------ before and after the products
 
-// Adds the partial sums of a split reduction in the order of the splits, then the epilogue:
-// 8 columns of a row per thread.
-__global__ void __launch_bounds__(256) muon_join_kernel(const __grid_constant__ JoinParams p) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int64_t groups = (p.e.cols + 7) / 8;
-  const int64_t total = groups * p.e.rows;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t m = i / groups, n = (i - m * groups) * 8;
-    const float* src = p.partial + m * p.ld_partial + n;
-    F2 v[4] = {0ull, 0ull, 0ull, 0ull};  // zeros
-#pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-      const float4 a = *reinterpret_cast<const float4*>(src + s * p.split_stride);
-      const float4 b = *reinterpret_cast<const float4*>(src + s * p.split_stride + 4);
-      v[0] = add2(v[0], pair(a.x, a.y));
-      v[1] = add2(v[1], pair(a.z, a.w));
-      v[2] = add2(v[2], pair(b.x, b.y));
-      v[3] = add2(v[3], pair(b.z, b.w));
-    }
-    finish_segment<8>(p.e, m, n, v);
-  }
+// Calls f(row, group of 8 columns) over the sweep, for block `b` of it.
+template <class F>
+__device__ __forceinline__ void run_sweep(const Sweep& s, int b, F&& f) {
+  const int along = 1 << s.shift, deep = 256 >> s.shift;
+  const int rb = b / s.col_blocks, cb = b - rb * s.col_blocks;
+  const int g0 = (cb << s.shift) + (threadIdx.x & (along - 1));
+  for (int64_t r = static_cast<int64_t>(rb) * deep + (threadIdx.x >> s.shift); r < s.rows;
+       r += static_cast<int64_t>(s.row_blocks) * deep)
+    for (int g = g0; g < s.groups; g += s.col_blocks << s.shift) f(r, g);
 }
-
-// ------------------------------------------------------------------ operands
 
 // x = h + m + l: each term takes the leading 8 bits of what is left, truncated, so the three
 // hold the 24 bits of an fp32 value exactly and none overflows (only terms below 2^-133 are
 // lost).  What is not finite goes into h alone.  A bf16 source is copied to rows that TMA can read.
-__global__ void __launch_bounds__(256) muon_pack_kernel(const __grid_constant__ PackParams p) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int64_t groups = p.ld_dst / 8;
-  const int64_t total = groups * p.rows;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t r = i / groups;
-    const int c = static_cast<int>(i - r * groups) * 8;
-    const EpiView src{const_cast<void*>(p.src), p.ld_src, p.src_bf16, p.vec};
-    float x[8];
-    load_segment<8>(src, r * p.ld_src + c, p.cols - c, x);
-    for (int t = 0; t < p.terms; ++t) {
-      uint32_t w[4];
+__device__ __forceinline__ void pack_group(const PackTask& p, int64_t r, int g) {
+  const int c = g * 8;
+  float x[8];
+  load_segment<8>(p.src, r * p.src.ld + c, p.cols - c, x);
+  for (int t = 0; t < p.terms; ++t) {
+    uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(x[j]);
-        uint32_t hi = b >> 16;
-        if ((b & 0x7F800000u) == 0x7F800000u) {
-          if (b & 0x007FFFFFu) hi |= 0x40u;  // a NaN stays one
-          x[j] = 0.f;
-        } else {
-          x[j] -= __uint_as_float(b & 0xFFFF0000u);
-        }
-        w[j >> 1] = (j & 1) ? (w[j >> 1] | (hi << 16)) : hi;
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = __float_as_uint(x[j]);
+      uint32_t hi = b >> 16;
+      if ((b & 0x7F800000u) == 0x7F800000u) {
+        if (b & 0x007FFFFFu) hi |= 0x40u;  // a NaN stays one
+        x[j] = 0.f;
+      } else {
+        x[j] -= __uint_as_float(b & 0xFFFF0000u);
       }
-      *reinterpret_cast<uint4*>(p.dst + t * p.term_stride + r * p.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      w[j >> 1] = (j & 1) ? (w[j >> 1] | (hi << 16)) : hi;
     }
+    *reinterpret_cast<uint4*>(p.dst + t * p.term_stride + r * p.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Sums of columns over the rows: block b takes 256 columns, 8 a thread, and every slices-th
+// group of 8 rows.
+__device__ __forceinline__ void column_sums(const ColumnSumTask& p, int b, float (*red)[256]) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int blocks = (p.cols + 255) / 256;
+  const int slice = b / blocks, c0 = (b - slice * blocks) * 256;
+  const int c = c0 + lane * 8;
+  F2 s[4] = {0ull, 0ull, 0ull, 0ull};  // zeros
+  if (c < p.cols) {
+#pragma unroll 4
+    for (int64_t r = slice * 8 + w; r < p.rows; r += int64_t(8) * p.slices) {
+      F2 x[4];
+      load_pairs<8>(p.src, r * p.src.ld + c, p.cols - c, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] = add2(s[j], x[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&red[w][lane * 8 + 2 * j]) = split(s[j]);
+  __syncthreads();
+  const int o = c0 + threadIdx.x;
+  if (o < p.cols) {
+    float t = red[0][threadIdx.x];
+    for (int k = 1; k < 8; ++k) t += red[k][threadIdx.x];
+    if (p.slices == 1)
+      p.out[o] = p.accumulate ? p.out[o] + t : t;
+    else
+      p.partial[static_cast<int64_t>(slice) * p.cols + o] = t;
+  }
+}
+
+__global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant__ PrepareParams p) {
+  __shared__ float red[8][256];
+  griddep_wait();
+  griddep_launch_dependents();
+  int i = 0;
+  while (static_cast<int>(blockIdx.x) >= p.begin[i + 1]) ++i;
+  const int b = static_cast<int>(blockIdx.x) - p.begin[i];
+  if (i < p.packs) {
+    const PackTask& t = p.pack[i];
+    run_sweep(t.sweep, b, [&](int64_t r, int g) { pack_group(t, r, g); });
+  } else {
+    column_sums(p.sum, b, red);
+  }
+}
+
+// Adds the partial sums of a split reduction in the order of the splits, then the epilogue.
+__device__ __forceinline__ void join_group(const JoinTask& p, int64_t m, int g) {
+  const int64_t n = static_cast<int64_t>(g) * 8;
+  const float* src = p.partial + m * p.ld_partial + n;
+  F2 v[4] = {0ull, 0ull, 0ull, 0ull};  // zeros
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float4 a = *reinterpret_cast<const float4*>(src + s * p.split_stride);
+    const float4 b = *reinterpret_cast<const float4*>(src + s * p.split_stride + 4);
+    v[0] = add2(v[0], pair(a.x, a.y));
+    v[1] = add2(v[1], pair(a.z, a.w));
+    v[2] = add2(v[2], pair(b.x, b.y));
+    v[3] = add2(v[3], pair(b.z, b.w));
+  }
+  finish_segment<8>(p.e, m, n, v);
+}
+
+// The slices of the column sums: 32 columns per block, 8 warps over the slices.
+__device__ __forceinline__ void join_column_sums(const ColumnSumTask& p, int b, float (*red)[32]) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = b * 32 + lane;
+  float t = 0.f;
+  if (c < p.cols) {
+#pragma unroll 4
+    for (int s = w; s < p.slices; s += 8) t += p.partial[static_cast<int64_t>(s) * p.cols + c];
+  }
+  red[w][lane] = t;
+  __syncthreads();
+  if (w == 0 && c < p.cols) {
+    for (int k = 1; k < 8; ++k) t += red[k][lane];
+    p.out[c] = p.accumulate ? p.out[c] + t : t;
+  }
+}
+
+__global__ void __launch_bounds__(256) muon_finish_kernel(const __grid_constant__ FinishParams p) {
+  __shared__ float red[8][32];
+  griddep_wait();
+  griddep_launch_dependents();
+  int i = 0;
+  while (static_cast<int>(blockIdx.x) >= p.begin[i + 1]) ++i;
+  const int b = static_cast<int>(blockIdx.x) - p.begin[i];
+  if (i < p.joins) {
+    const JoinTask& t = p.join[i];
+    run_sweep(t.sweep, b, [&](int64_t r, int g) { join_group(t, r, g); });
+  } else {
+    join_column_sums(p.sum, b, red);
   }
 }
 
 // ------------------------------------------------------------------ launches
-
-template <class K, class P>
-static cudaError_t launch_dependent(K kernel, const P& p, unsigned blocks, unsigned threads, int smem, int cluster,
-                                    cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
 
 template <class L>
 static cudaError_t launch_tiles(const ProductParams& p, int sms, cudaStream_t stream) {
@@ -592,8 +651,8 @@ static cudaError_t launch_tiles(const ProductParams& p, int sms, cudaStream_t st
     configured_device = dev;
   }
   const int units = p.tiles_m * p.tiles_n * p.splits;
-  return launch_dependent(kernel, p, static_cast<unsigned>(L::CG * std::min(units, resident)), L::kThreads,
-                          L::kSmemBytes, L::CG, stream);
+  return launch_dependent(kernel, p, dim3(static_cast<unsigned>(L::CG * std::min(units, resident))), L::kThreads,
+                          stream, L::kSmemBytes, L::CG);
 }
 
 using Pair256 = Product<2, 256, false, false>;
@@ -624,16 +683,12 @@ cudaError_t launch_product(int tile, const ProductParams& p, int sms, cudaStream
   }
 }
 
-static unsigned loop_blocks(int64_t items, int sms) {
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, 256), int64_t(sms) * 16)));
+cudaError_t launch_prepare(const PrepareParams& p, cudaStream_t stream) {
+  return launch_dependent(muon_prepare_kernel, p, dim3(static_cast<unsigned>(p.begin[p.packs + 1])), 256, stream);
 }
 
-cudaError_t launch_join(const JoinParams& p, int sms, cudaStream_t stream) {
-  return launch_dependent(muon_join_kernel, p, loop_blocks(ceil_div(p.e.cols, 8) * p.e.rows, sms), 256, 0, 1, stream);
-}
-
-cudaError_t launch_pack(const PackParams& p, int sms, cudaStream_t stream) {
-  return launch_dependent(muon_pack_kernel, p, loop_blocks(p.ld_dst / 8 * p.rows, sms), 256, 0, 1, stream);
+cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream) {
+  return launch_dependent(muon_finish_kernel, p, dim3(static_cast<unsigned>(p.begin[p.joins + 1])), 256, stream);
 }
 
 }  // namespace muon

@@ -52,6 +52,7 @@ struct ProductParams {
   uint8_t seg_a[8], seg_b[8]; // the terms of each segment, smallest products first
   float* partial;             // [splits][e.rows][ld_partial] for the join kernel, or nullptr
   int64_t ld_partial, split_stride;
+  int32_t beside;             // runs beside the product launched before it (see the kernel)
   unsigned long long timeout_ns;
 };
 
@@ -62,20 +63,90 @@ int product_tile_m(int tile);
 int product_tile_n(int tile);
 cudaError_t launch_product(int tile, const ProductParams& p, int sms, cudaStream_t stream);
 
-struct JoinParams {
+// How 256-thread blocks cover rows x groups of 8 columns: 2^shift threads along a row.
+struct Sweep {
+  int64_t rows;
+  int32_t groups, shift;
+  int32_t row_blocks, col_blocks;
+};
+
+inline Sweep make_sweep(int64_t rows, int64_t groups, int64_t most_blocks) {
+  Sweep s{rows, static_cast<int32_t>(groups), 0, 1, 1};
+  while (s.shift < 8 && (int64_t(1) << s.shift) < groups) ++s.shift;
+  const int64_t rb = (rows + (256 >> s.shift) - 1) / (256 >> s.shift);
+  s.row_blocks = static_cast<int32_t>(rb < most_blocks ? rb : most_blocks);
+  const int64_t cb = (groups + (int64_t(1) << s.shift) - 1) >> s.shift, room = most_blocks / s.row_blocks;
+  s.col_blocks = static_cast<int32_t>(cb < room ? cb : room > 1 ? room : 1);
+  return s;
+}
+
+inline int sweep_blocks(const Sweep& s) { return s.row_blocks * s.col_blocks; }
+
+// An operand laid out for the tensor cores: [terms][sweep.rows][ld_dst].
+struct PackTask {
+  EpiView src;
+  __nv_bfloat16* dst;
+  int64_t ld_dst, term_stride;
+  int32_t cols, terms;
+  Sweep sweep;
+};
+
+// Column sums of a matrix, in `slices` partial sums over its rows.
+struct ColumnSumTask {
+  EpiView src;
+  float* out;
+  float* partial;  // [slices][cols]
+  int64_t rows;
+  int32_t cols, accumulate, slices;
+};
+
+// What precedes the products of a call, in one launch: blocks [begin[i], begin[i + 1]) run
+// task i, the column sums last.
+struct PrepareParams {
+  PackTask pack[3];
+  ColumnSumTask sum;
+  int32_t packs;
+  int32_t begin[5];
+};
+
+// The end of a split reduction.
+struct JoinTask {
   Epilogue e;
   const float* partial;
   int64_t ld_partial, split_stride;
   int32_t splits;
+  Sweep sweep;
 };
-cudaError_t launch_join(const JoinParams& p, int sms, cudaStream_t stream);
 
-struct PackParams {
-  const void* src;
-  __nv_bfloat16* dst;  // [terms][rows][ld_dst]
-  int64_t rows, ld_src, ld_dst, term_stride;
-  int32_t cols, src_bf16, terms, vec;
+// What follows the products, likewise.
+struct FinishParams {
+  JoinTask join[2];
+  ColumnSumTask sum;
+  int32_t joins;
+  int32_t begin[4];
 };
-cudaError_t launch_pack(const PackParams& p, int sms, cudaStream_t stream);
+
+cudaError_t launch_prepare(const PrepareParams& p, cudaStream_t stream);
+cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream);
+
+// Launches with programmatic stream serialisation: every kernel of the layers waits
+// (griddepcontrol.wait) before it touches what the launch before may have written.
+template <class K, class P>
+cudaError_t launch_dependent(K kernel, const P& p, dim3 grid, int threads, cudaStream_t stream, int smem = 0,
+                             int cluster = 1) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 }  // namespace muon
