@@ -99,25 +99,34 @@ struct Plan {
 
 int segments(int ta, int tb) { return ta == 1 ? tb : (tb == 1 ? ta : kMaxSegments); }
 
+// What a plan depends on besides the sizes.
+struct PlanTraits {
+  int nseg;      // term products
+  bool sum;      // some output is fp32
+  bool tokens;   // the output's rows are tokens
+  bool aligned;  // the epilogue's rows can be accessed 16 bytes at a time
+};
+
 // Picks the tile and the number of splits with the least estimated time, in SM cycles:
 // waves of units times their k-blocks, and for a split the partial sums' way out and back.
-// sum: some output is fp32.
-Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool may_flip) {
+Plan search_plan(int64_t m, int64_t n, int64_t k, const PlanTraits& t) {
   Plan best;
   double least = 1e30;
   const int64_t nk = ceil_div(k, kProductBK);
+  const bool few = t.tokens && m <= kFlipTokens;
   for (int tile = kPair256; tile <= kFlip64; ++tile) {
-    if (tile == (sum ? kPair256 : kPair256Sum)) continue;
-    const bool flip = tile >= kFlip32;
-    if (flip && (!may_flip || m > product_tile_n(tile))) continue;
-    if (!flip && may_flip && m <= kFlipTokens) continue;
-    const int64_t tm = ceil_div(flip ? n : m, product_tile_m(tile)), tn = ceil_div(flip ? m : n, product_tile_n(tile));
-    const int64_t workers = tile <= kPair256Sum ? kSms / 2 : kSms;
-    const double block = (tile <= kPair256Sum ? 512.0 : tile == kOne128 ? 450.0 : 320.0) * nseg;
+    const TileShape& shape = kTileShapes[tile];
+    if (shape.ctas == 2 && shape.sum != t.sum) continue;
+    if ((tile >= kFlip32) != few || (few && m > shape.n)) continue;
+    const int64_t tm = ceil_div(shape.flip ? n : m, shape.m), tn = ceil_div(shape.flip ? m : n, shape.n);
+    const int64_t workers = kSms / shape.ctas;
+    const double block = (shape.ctas == 2 ? 512.0 : few ? 320.0 : 450.0) * t.nseg;
     if (tm * tn > 0x3fffffff) continue;
     for (int64_t want = 1; want <= 32; ++want) {
       const int64_t per = ceil_div(nk, want), splits = ceil_div(nk, per);
       if (splits != want || (want > 1 && per < 2) || tm * tn * splits > 0x3fffffff) continue;
+      // (partial sums are aligned whatever the output is)
+      if (!few && shape.flip != (!t.aligned && splits == 1)) continue;
       const double waves = static_cast<double>(ceil_div(tm * tn * splits, workers));
       double cost = waves * (per * block + 600.0) + 3000.0;
       if (splits > 1) cost += 3500.0 + static_cast<double>(splits + 1) * m * n * 4.0 / 3000.0;
@@ -132,7 +141,7 @@ Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool may_f
     }
   }
   best.nk = nk;
-  best.nseg = nseg;
+  best.nseg = t.nseg;
   if (best.splits > 1) {
     best.ld_partial = ceil_div(n, 32) * 32;
     best.partial_bytes = up(static_cast<size_t>(best.splits) * m * best.ld_partial * 4);
@@ -142,20 +151,20 @@ Plan search_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool may_f
 
 // The search takes a microsecond or two; a call asks for its plan twice (its workspace, then
 // itself), and a training loop for the same few sizes again and again.
-Plan make_plan(int64_t m, int64_t n, int64_t k, int nseg, bool sum, bool may_flip) {
+Plan make_plan(int64_t m, int64_t n, int64_t k, const PlanTraits& t) {
   struct Entry {
     int64_t m = -1, n = 0, k = 0;
     int flags = 0;
     Plan plan;
   };
   static thread_local Entry table[64];
-  const int flags = nseg * 4 + (sum ? 2 : 0) + (may_flip ? 1 : 0);
+  const int flags = t.nseg * 8 + (t.sum ? 4 : 0) + (t.tokens ? 2 : 0) + (t.aligned ? 1 : 0);
   uint64_t h = static_cast<uint64_t>(m) * 0x9E3779B97F4A7C15ull;
   h = (h ^ static_cast<uint64_t>(n)) * 0x9E3779B97F4A7C15ull;
   h = (h ^ static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull;
   Entry& e = table[((h >> 32) ^ static_cast<uint64_t>(flags)) % 64];
   if (e.m != m || e.n != n || e.k != k || e.flags != flags) {
-    e.plan = search_plan(m, n, k, nseg, sum, may_flip);
+    e.plan = search_plan(m, n, k, t);
     e.m = m;
     e.n = n;
     e.k = k;
@@ -200,13 +209,14 @@ bool plain_epilogue(const Epilogue& e) {
 muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const Epilogue& e,
                           uint8_t* ws, size_t partial_at, bool beside, FinishParams* finish, cudaStream_t s) {
   static const uint8_t both_a[kMaxSegments] = {0, 2, 1, 0, 1, 0}, both_b[kMaxSegments] = {2, 0, 1, 1, 0, 0};
-  const bool flip = pl.tile >= kFlip32;
+  const TileShape& shape = kTileShapes[pl.tile];
+  const bool flip = shape.flip;
   const Operand &am = flip ? b : a, &bm = flip ? a : b;
   ProductParams p{};
   p.a_mn = flip ? b_mn : a_mn;
   p.b_mn = flip ? a_mn : b_mn;
   if (!operand_maps(p.map_a, am, ws, p.a_mn, 128) ||
-      !operand_maps(p.map_b, bm, ws, p.b_mn, pl.tile <= kPair256Sum ? 128 : product_tile_n(pl.tile)))
+      !operand_maps(p.map_b, bm, ws, p.b_mn, shape.n / shape.ctas))
     return MUON_ERR_CUDA;
   p.e = e;
   p.e.plain = plain_epilogue(e);
@@ -215,7 +225,7 @@ muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Ope
   p.nk = static_cast<int32_t>(pl.nk);
   p.splits = static_cast<int32_t>(pl.splits);
   p.kb_per_split = static_cast<int32_t>(pl.kb_per_split);
-  p.piece = pl.tile == kPair256 ? p.kb_per_split : static_cast<int32_t>(kPieceBlocks);
+  p.piece = shape.sum ? static_cast<int32_t>(kPieceBlocks) : p.kb_per_split;
   p.nseg = pl.nseg;
   for (int g = 0; g < pl.nseg; ++g) {  // the smallest products first
     p.seg_a[g] = static_cast<uint8_t>(am.terms == 1 ? 0 : bm.terms == 1 ? pl.nseg - 1 - g : both_a[g]);
@@ -240,6 +250,11 @@ muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Ope
   return queued(launch_product(pl.tile, p, kSms, s));
 }
 
+// Whether the rows of an epilogue operand (if it is there) can be accessed 16 bytes at a time.
+bool wide_rows(const muon_view_t& v, int64_t rows, int64_t cols) {
+  return v.data == nullptr || epi_view(v, rows, cols).vec > 0;
+}
+
 bool wants_sum(const muon_view_t& out) { return out.data != nullptr && out.dtype == MUON_F32; }
 
 struct LinearPlan {
@@ -253,8 +268,10 @@ LinearPlan plan_linear(const muon_linear_t* d) {
   if (d->rows == 0) return pl;
   pl.x = Operand(d->x, d->rows, d->in);
   pl.w = Operand(d->w, d->out, d->in);
-  pl.z = make_plan(d->rows, d->out, d->in, segments(pl.x.terms, pl.w.terms), wants_sum(d->y) || wants_sum(d->preact),
-                   true);
+  const bool aligned = wide_rows(d->y, d->rows, d->out) && wide_rows(d->preact, d->rows, d->out) &&
+                       wide_rows(d->residual, d->rows, d->out);
+  pl.z = make_plan(d->rows, d->out, d->in, {segments(pl.x.terms, pl.w.terms),
+                                            wants_sum(d->y) || wants_sum(d->preact), true, aligned});
   pl.x.place(&pl.bytes);
   pl.w.place(&pl.bytes);
   pl.partial_at = pl.bytes;
@@ -278,14 +295,17 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
   if (dx) {
     pl.w = Operand(d->w, d->out, d->in);
     pl.w.place(&pl.bytes);
-    pl.dx = make_plan(d->rows, d->in, d->out, segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), true);
+    const bool aligned = wide_rows(d->dx, d->rows, d->in) && wide_rows(d->skip, d->rows, d->in) &&
+                         (d->in_act == MUON_ACT_NONE || wide_rows(d->preact, d->rows, d->in));
+    pl.dx = make_plan(d->rows, d->in, d->out, {segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), true, aligned});
     pl.dx_at = pl.bytes;
     pl.bytes += pl.dx.partial_bytes;
   }
   if (dw) {
     pl.x = Operand(d->x, d->rows, d->in);
     pl.x.place(&pl.bytes);
-    pl.dw = make_plan(d->out, d->in, d->rows, segments(pl.dy.terms, pl.x.terms), true, false);
+    pl.dw = make_plan(d->out, d->in, d->rows, {segments(pl.dy.terms, pl.x.terms), true, false,
+                                               wide_rows(d->dw, d->out, d->in)});
     pl.dw_at = pl.bytes;
     pl.bytes += pl.dw.partial_bytes;
   }

@@ -257,8 +257,9 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
               uint8_t* sa = smem + s * L::kStageBytes;
               if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * L::kStageBytes);
               const uint32_t fb = full0 + 8u * static_cast<uint32_t>(s);
-              load_operand<CG, 128>(sa, ma, p.a_mn, a0, kb * L::BK, &full[s], fb);
-              load_operand<CG, L::TNB>(sa + L::kABytes, mb, p.b_mn, b0, kb * L::BK, &full[s], fb);
+              const int k0 = kb * L::BK;
+              load_operand<CG, 128>(sa, ma, p.a_mn, a0, k0, &full[s], fb);
+              load_operand<CG, L::TNB>(sa + L::kABytes, mb, p.b_mn, b0, k0, &full[s], fb);
               ++issued;
               if (++s == S) {
                 s = 0;
@@ -655,30 +656,19 @@ static cudaError_t launch_tiles(const ProductParams& p, int sms, cudaStream_t st
                           stream, L::kSmemBytes, L::CG);
 }
 
-using Pair256 = Product<2, 256, false, false>;
-using Pair256Sum = Product<2, 256, true, false>;
-using One128 = Product<1, 128, true, false>;
-using Flip32 = Product<1, 32, true, true>;
-using Flip64 = Product<1, 64, true, true>;
-
-int product_tile_m(int tile) { return tile <= kPair256Sum ? 256 : 128; }
-
-int product_tile_n(int tile) {
-  switch (tile) {
-    case kOne128: return 128;
-    case kFlip32: return 32;
-    case kFlip64: return 64;
-    default: return 256;
-  }
-}
+template <int TILE>
+using ProductOf = Product<kTileShapes[TILE].ctas, kTileShapes[TILE].n, kTileShapes[TILE].sum, kTileShapes[TILE].flip>;
 
 cudaError_t launch_product(int tile, const ProductParams& p, int sms, cudaStream_t stream) {
   switch (tile) {
-    case kPair256: return launch_tiles<Pair256>(p, sms, stream);
-    case kPair256Sum: return launch_tiles<Pair256Sum>(p, sms, stream);
-    case kOne128: return launch_tiles<One128>(p, sms, stream);
-    case kFlip32: return launch_tiles<Flip32>(p, sms, stream);
-    case kFlip64: return launch_tiles<Flip64>(p, sms, stream);
+    case kPair256: return launch_tiles<ProductOf<kPair256>>(p, sms, stream);
+    case kPair256Sum: return launch_tiles<ProductOf<kPair256Sum>>(p, sms, stream);
+    case kOne128: return launch_tiles<ProductOf<kOne128>>(p, sms, stream);
+    case kFlipPair256: return launch_tiles<ProductOf<kFlipPair256>>(p, sms, stream);
+    case kFlipPair256Sum: return launch_tiles<ProductOf<kFlipPair256Sum>>(p, sms, stream);
+    case kFlip128: return launch_tiles<ProductOf<kFlip128>>(p, sms, stream);
+    case kFlip32: return launch_tiles<ProductOf<kFlip32>>(p, sms, stream);
+    case kFlip64: return launch_tiles<ProductOf<kFlip64>>(p, sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }

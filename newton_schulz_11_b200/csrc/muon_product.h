@@ -31,12 +31,30 @@ constexpr int kTerms = 3;                // bf16 terms of an fp32 operand
 constexpr int kMaxSegments = 6;          // products of two such operands that are kept
 constexpr int kProductBK = 64;           // reduction depth of a k-block
 
+// How a product is tiled.  The flipped tiles hold the output's columns on their M side (the
+// lanes of tensor memory), so that a warp's 32 lanes are neighbouring columns of one row:
+// they take few tokens, whose tile would be mostly empty the other way round, and outputs
+// whose rows cannot be accessed 16 bytes at a time, element by element in whole lines.
 enum ProductTile : int {
   kPair256 = 0,     // 256 x 256 on a CTA pair, the whole reduction in tensor memory
-  kPair256Sum = 1,  // the same, the reduction in pieces that are added in registers
-  kOne128 = 2,      // 128 x 128 on one CTA, in pieces
-  kFlip32 = 3,      // few tokens: 128 features x 32 tokens on one CTA, in pieces
-  kFlip64 = 4,      // 128 features x 64 tokens
+  kPair256Sum,      // the same, the reduction in pieces that are added in registers
+  kOne128,          // 128 x 128 on one CTA, in pieces
+  kFlipPair256,     // as the first three
+  kFlipPair256Sum,
+  kFlip128,
+  kFlip32,          // 128 columns x 32 tokens on one CTA, in pieces
+  kFlip64,          // 128 columns x 64 tokens
+};
+
+struct TileShape {
+  int m, n;    // rows and columns of the tile
+  int ctas;
+  bool flip, sum;
+};
+
+constexpr TileShape kTileShapes[] = {
+    {256, 256, 2, false, false}, {256, 256, 2, false, true}, {128, 128, 1, false, true}, {256, 256, 2, true, false},
+    {256, 256, 2, true, true},   {128, 128, 1, true, true},  {128, 32, 1, true, true},   {128, 64, 1, true, true},
 };
 
 struct ProductParams {
@@ -59,8 +77,6 @@ struct ProductParams {
 // bf16 operand map of a matrix with rows of ld elements: boxes of 64 columns x box_rows rows.
 bool encode_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 
-int product_tile_m(int tile);
-int product_tile_n(int tile);
 cudaError_t launch_product(int tile, const ProductParams& p, int sms, cudaStream_t stream);
 
 // How 256-thread blocks cover rows x groups of 8 columns: 2^shift threads along a row.
