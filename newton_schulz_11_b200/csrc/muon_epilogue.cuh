@@ -7,51 +7,73 @@
 
 namespace muon {
 
+// N 32-bit words from byte address `a`, which need not be aligned to 16: the 16-byte units
+// that hold them, shifted into place.  Units from `end` on (the end of the row) are not
+// touched; their words are zero.  HALVES: `a` is a multiple of 2, else of 4.
+template <int N, bool HALVES>
+__device__ __forceinline__ void load_shifted(uintptr_t a, uintptr_t end, uint32_t (&x)[N]) {
+  const uint32_t o = static_cast<uint32_t>(a & 15u);
+  const uintptr_t u = a - o;
+  uint32_t w[N + 4];
+#pragma unroll
+  for (int i = 0; i < N / 4 + 1; ++i) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if ((i < N / 4 || o != 0) && u + 16 * i < end) v = *reinterpret_cast<const uint4*>(u + 16 * i);
+    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+  }
+  if (o & 8u) {
+#pragma unroll
+    for (int i = 0; i < N + 2; ++i) w[i] = w[i + 2];
+  }
+  if (o & 4u) {
+#pragma unroll
+    for (int i = 0; i < N + 1; ++i) w[i] = w[i + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = HALVES && (o & 2u) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+}
+
 // NC (a multiple of 8) consecutive elements of a row, the first `valid` of them; the rest
 // are left at zero.  `off` is the element offset of the segment.
 template <int NC>
 __device__ __forceinline__ void load_segment(const EpiView& v, int64_t off, int valid, float (&x)[NC]) {
-  if (valid >= NC && v.vec) {
-    if (v.bf16) {
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(v.p) + off;
-      uint4 w[NC / 8];
-      if (NC % 16 == 0 && v.vec == 2) {
+  const bool whole = valid >= NC && v.vec != 0;
+  if (v.bf16) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(v.p) + off;
 #pragma unroll
-        for (int i = 0; i < NC / 16; ++i) ld_global_v8(p + 16 * i, w[2 * i], w[(2 * i + 1) % (NC / 8)]);
+    for (int h = 0; h < NC / 8; ++h) {
+      uint32_t q[4];
+      if (whole) {
+        const uint4 w = reinterpret_cast<const uint4*>(p)[h];
+        q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
       } else {
-#pragma unroll
-        for (int i = 0; i < NC / 8; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+        load_shifted<4, true>(reinterpret_cast<uintptr_t>(p + 8 * h), reinterpret_cast<uintptr_t>(p + valid), q);
       }
 #pragma unroll
-      for (int i = 0; i < NC / 8; ++i) {
-        const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[8 * i + 2 * j] = __uint_as_float(q[j] << 16);
-          x[8 * i + 2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
-        }
-      }
-    } else {
-      const float* p = static_cast<const float*>(v.p) + off;
-      uint4 w[NC / 4];
-      if (v.vec == 2) {
-#pragma unroll
-        for (int i = 0; i < NC / 8; ++i) ld_global_v8(p + 8 * i, w[2 * i], w[2 * i + 1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NC / 4; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
-      }
-#pragma unroll
-      for (int i = 0; i < NC / 4; ++i) {
-        x[4 * i] = __uint_as_float(w[i].x);
-        x[4 * i + 1] = __uint_as_float(w[i].y);
-        x[4 * i + 2] = __uint_as_float(w[i].z);
-        x[4 * i + 3] = __uint_as_float(w[i].w);
+      for (int j = 0; j < 4; ++j) {
+        x[8 * h + 2 * j] = __uint_as_float(q[j] << 16);
+        x[8 * h + 2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
       }
     }
   } else {
+    const float* p = static_cast<const float*>(v.p) + off;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) x[j] = j < valid ? load_elem(v.p, off + j, v.bf16) : 0.f;
+    for (int h = 0; h < NC / 8; ++h) {
+      uint32_t q[8];
+      if (whole && v.vec == 2) {
+        uint4 a, b;
+        ld_global_v8(p + 8 * h, a, b);
+        q[0] = a.x, q[1] = a.y, q[2] = a.z, q[3] = a.w, q[4] = b.x, q[5] = b.y, q[6] = b.z, q[7] = b.w;
+      } else {
+        load_shifted<8, false>(reinterpret_cast<uintptr_t>(p + 8 * h), reinterpret_cast<uintptr_t>(p + valid), q);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[8 * h + j] = __uint_as_float(q[j]);
+    }
+  }
+  if (valid < NC) {  // what shares a unit with the row's end
+#pragma unroll
+    for (int j = 0; j < NC; ++j) x[j] = j < valid ? x[j] : 0.f;
   }
 }
 

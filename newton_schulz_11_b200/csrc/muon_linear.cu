@@ -93,8 +93,10 @@ struct Plan {
   int tile = kOne128;
   int64_t tiles_m = 0, tiles_n = 0, nk = 0, splits = 1, kb_per_split = 0;
   int nseg = 1;
+  bool shared = false;  // launched with the call's other product
   size_t partial_bytes = 0;
   int64_t ld_partial = 0;
+  double cost = 0.0;
 };
 
 int segments(int ta, int tb) { return ta == 1 ? tb : (tb == 1 ? ta : kMaxSegments); }
@@ -107,46 +109,88 @@ struct PlanTraits {
   bool aligned;  // the epilogue's rows can be accessed 16 bytes at a time
 };
 
-// Picks the tile and the number of splits with the least estimated time, in SM cycles:
-// waves of units times their k-blocks, and for a split the partial sums' way out and back.
+// The estimated time of a product in SM cycles, fitted to measurements (captured calls, us):
+//   a k-block of 64 takes a CTA or a pair about 0.4 us of 128 x 128 or 256 x 256 alike, since
+//   both wait for 32 KB a CTA: 1024 x 1024 x 8192 in 64 single tiles 54, in 16 pair tiles 55;
+//   a split of a large product costs about 3 us and its traffic: 1024 x 1024 x 8192 takes 55,
+//   35, 24.7, 30.8 in 1, 2, 4 and 8 splits; 2048 x 1024 x 1024 takes 11.0, and 15.3 in 2.
+double pair_cost(const TileShape& shape, int64_t tiles, int64_t splits, int64_t per, int64_t outputs, int nseg) {
+  double start = shape.sum ? 2200.0 : 1500.0;
+  if (shape.flip) start += 5000.0;  // 128 outputs a thread, one by one
+  const double waves = static_cast<double>(ceil_div(tiles * splits, kSms / 2));
+  const double cost = waves * (static_cast<double>(per) * 760.0 * nseg + start);
+  return splits == 1 ? cost : cost + 5500.0 + static_cast<double>((splits + 1) * outputs) * 4.0 / 2600.0;
+}
+
+//   a small product has its launch's start and its epilogue, which the cluster divides
+double small_cost(const TileShape& shape, int64_t tiles, int64_t cluster, int64_t nk, int nseg) {
+  const double waves = static_cast<double>(ceil_div(tiles * cluster, kSms));
+  const double block = shape.n == 128 ? 760.0 : 700.0;
+  return waves * (static_cast<double>(ceil_div(nk, cluster)) * block * nseg + 2500.0 + 30.0 * shape.n / cluster) +
+         (cluster > 1 ? 1000.0 : 0.0);
+}
+
+// Picks the tile and the number of splits with the least estimated time.
 Plan search_plan(int64_t m, int64_t n, int64_t k, const PlanTraits& t) {
   Plan best;
-  double least = 1e30;
-  const int64_t nk = ceil_div(k, kProductBK);
+  best.cost = 1e30;
+  best.nk = ceil_div(k, kProductBK);
+  best.nseg = t.nseg;
   const bool few = t.tokens && m <= kFlipTokens;
   for (int tile = kPair256; tile <= kFlip64; ++tile) {
     const TileShape& shape = kTileShapes[tile];
-    if (shape.ctas == 2 && shape.sum != t.sum) continue;
-    if ((tile >= kFlip32) != few || (few && m > shape.n)) continue;
+    if (shape.pair && (shape.sum != t.sum || few)) continue;
+    if (tile >= kFlip32 ? !few || m > shape.n : few) continue;
     const int64_t tm = ceil_div(shape.flip ? n : m, shape.m), tn = ceil_div(shape.flip ? m : n, shape.n);
-    const int64_t workers = kSms / shape.ctas;
-    const double block = (shape.ctas == 2 ? 512.0 : few ? 320.0 : 450.0) * t.nseg;
-    if (tm * tn > 0x3fffffff) continue;
-    for (int64_t want = 1; want <= 32; ++want) {
-      const int64_t per = ceil_div(nk, want), splits = ceil_div(nk, per);
-      if (splits != want || (want > 1 && per < 2) || tm * tn * splits > 0x3fffffff) continue;
+    for (int64_t want = 1; want <= (shape.pair ? 32 : 8); shape.pair ? ++want : want *= 2) {
+      const int64_t per = ceil_div(best.nk, want);
+      if (tm * tn * want > 0x3fffffff) break;
       // (partial sums are aligned whatever the output is)
-      if (!few && shape.flip != (!t.aligned && splits == 1)) continue;
-      const double waves = static_cast<double>(ceil_div(tm * tn * splits, workers));
-      double cost = waves * (per * block + 600.0) + 3000.0;
-      if (splits > 1) cost += 3500.0 + static_cast<double>(splits + 1) * m * n * 4.0 / 3000.0;
-      if (cost < least) {
-        least = cost;
+      const bool flip = !t.aligned && (!shape.pair || want == 1);
+      if (!few && shape.flip != flip) continue;
+      if (shape.pair ? (ceil_div(best.nk, per) != want || (want > 1 && per < 2)) : want > best.nk) continue;
+      const double cost = shape.pair ? pair_cost(shape, tm * tn, want, per, m * n, t.nseg)
+                                     : small_cost(shape, tm * tn, want, best.nk, t.nseg);
+      if (cost < best.cost) {
+        best.cost = cost;
         best.tile = tile;
         best.tiles_m = tm;
         best.tiles_n = tn;
-        best.splits = splits;
+        best.splits = want;
         best.kb_per_split = per;
       }
     }
   }
-  best.nk = nk;
-  best.nseg = t.nseg;
-  if (best.splits > 1) {
+  if (kTileShapes[best.tile].pair && best.splits > 1) {
     best.ld_partial = ceil_div(n, 32) * 32;
     best.partial_bytes = up(static_cast<size_t>(best.splits) * m * best.ld_partial * 4);
   }
   return best;
+}
+
+// Two products of a call as small ones in one launch, where that beats one after the other
+// (their times and a launch of about 3000 cycles between them).
+void share_launch(Plan* a, int64_t am, int64_t an, Plan* b, int64_t bm, int64_t bn, bool aligned) {
+  const int tile = aligned ? kOne128 : kFlip128;
+  const TileShape& shape = kTileShapes[tile];
+  const int64_t atm = ceil_div(aligned ? am : an, 128), atn = ceil_div(aligned ? an : am, 128);
+  const int64_t btm = ceil_div(aligned ? bm : bn, 128), btn = ceil_div(aligned ? bn : bm, 128);
+  double least = a->cost + b->cost + 3000.0;
+  for (int64_t c = 1; c <= 8; c *= 2) {
+    if (c > std::min(a->nk, b->nk) || (atm * atn + btm * btn) * c > kSms) break;
+    const double cost = std::max(small_cost(shape, atm * atn, c, a->nk, a->nseg),
+                                 small_cost(shape, btm * btn, c, b->nk, b->nseg));
+    if (cost >= least) continue;
+    least = cost;
+    a->shared = b->shared = true;
+    a->tile = b->tile = tile;
+    a->splits = b->splits = c;
+    a->tiles_m = atm;
+    a->tiles_n = atn;
+    b->tiles_m = btm;
+    b->tiles_n = btn;
+    a->partial_bytes = b->partial_bytes = 0;
+  }
 }
 
 // The search takes a microsecond or two; a call asks for its plan twice (its workspace, then
@@ -205,18 +249,18 @@ bool plain_epilogue(const Epilogue& e) {
 }
 
 // a: the operand on the output's row side; b: on its column side.  mn: contiguous along the
-// side.  A split reduction leaves its end to `finish`.
-muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const Epilogue& e,
-                          uint8_t* ws, size_t partial_at, bool beside, FinishParams* finish, cudaStream_t s) {
+// side.  A split large product leaves its end to `finish`.
+muon_status_t make_product(const Plan& pl, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const Epilogue& e,
+                           uint8_t* ws, size_t partial_at, FinishParams* finish, ProductParams* out) {
   static const uint8_t both_a[kMaxSegments] = {0, 2, 1, 0, 1, 0}, both_b[kMaxSegments] = {2, 0, 1, 1, 0, 0};
   const TileShape& shape = kTileShapes[pl.tile];
   const bool flip = shape.flip;
   const Operand &am = flip ? b : a, &bm = flip ? a : b;
-  ProductParams p{};
+  ProductParams& p = *out;
   p.a_mn = flip ? b_mn : a_mn;
   p.b_mn = flip ? a_mn : b_mn;
   if (!operand_maps(p.map_a, am, ws, p.a_mn, 128) ||
-      !operand_maps(p.map_b, bm, ws, p.b_mn, shape.n / shape.ctas))
+      !operand_maps(p.map_b, bm, ws, p.b_mn, shape.pair ? 128 : shape.n))
     return MUON_ERR_CUDA;
   p.e = e;
   p.e.plain = plain_epilogue(e);
@@ -231,9 +275,8 @@ muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Ope
     p.seg_a[g] = static_cast<uint8_t>(am.terms == 1 ? 0 : bm.terms == 1 ? pl.nseg - 1 - g : both_a[g]);
     p.seg_b[g] = static_cast<uint8_t>(bm.terms == 1 ? 0 : am.terms == 1 ? pl.nseg - 1 - g : both_b[g]);
   }
-  p.beside = beside ? 1 : 0;
   p.timeout_ns = layers_wait_ns();
-  if (pl.splits > 1) {
+  if (shape.pair && pl.splits > 1) {
     p.partial = reinterpret_cast<float*>(ws + partial_at);
     p.ld_partial = pl.ld_partial;
     p.split_stride = e.rows * pl.ld_partial;
@@ -247,7 +290,16 @@ muon_status_t run_product(const Plan& pl, const Operand& a, bool a_mn, const Ope
     finish->begin[finish->joins + 1] = finish->begin[finish->joins] + sweep_blocks(j.sweep);
     ++finish->joins;
   }
-  return queued(launch_product(pl.tile, p, kSms, s));
+  return MUON_OK;
+}
+
+int small_blocks(const Plan& pl) { return static_cast<int>(pl.tiles_m * pl.tiles_n * pl.splits); }
+
+// Launches p (already made), or two small products that share a launch.
+muon_status_t run_product(const Plan& pl, const ProductGroup& g, const Plan* second, cudaStream_t s) {
+  if (kTileShapes[pl.tile].pair) return queued(launch_product_pair(pl.tile, g.p[0], kSms, s));
+  const int blocks = g.first_blocks + (second == nullptr ? 0 : small_blocks(*second));
+  return queued(launch_product_small(pl.tile, g, blocks, s));
 }
 
 // Whether the rows of an epilogue operand (if it is there) can be accessed 16 bytes at a time.
@@ -290,27 +342,30 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
   LinearGradPlan pl;
   if (d->rows == 0) return pl;
   const bool dx = d->dx.data != nullptr, dw = d->dw.data != nullptr;
+  bool dx_aligned = true;
   pl.dy = Operand(d->dy, d->rows, d->out);
   if (dx || dw) pl.dy.place(&pl.bytes);
   if (dx) {
     pl.w = Operand(d->w, d->out, d->in);
     pl.w.place(&pl.bytes);
-    const bool aligned = wide_rows(d->dx, d->rows, d->in) && wide_rows(d->skip, d->rows, d->in) &&
-                         (d->in_act == MUON_ACT_NONE || wide_rows(d->preact, d->rows, d->in));
-    pl.dx = make_plan(d->rows, d->in, d->out, {segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), true, aligned});
-    pl.dx_at = pl.bytes;
-    pl.bytes += pl.dx.partial_bytes;
+    dx_aligned = wide_rows(d->dx, d->rows, d->in) && wide_rows(d->skip, d->rows, d->in) &&
+                 (d->in_act == MUON_ACT_NONE || wide_rows(d->preact, d->rows, d->in));
+    pl.dx = make_plan(d->rows, d->in, d->out, {segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), true, dx_aligned});
   }
   if (dw) {
     pl.x = Operand(d->x, d->rows, d->in);
     pl.x.place(&pl.bytes);
     pl.dw = make_plan(d->out, d->in, d->rows, {segments(pl.dy.terms, pl.x.terms), true, false,
                                                wide_rows(d->dw, d->out, d->in)});
+    const bool same = wide_rows(d->dw, d->out, d->in) == dx_aligned;
+    if (dx && same) share_launch(&pl.dx, d->rows, d->in, &pl.dw, d->out, d->in, dx_aligned);
     pl.dw_at = pl.bytes;
     pl.bytes += pl.dw.partial_bytes;
   }
+  pl.dx_at = pl.bytes;
+  pl.bytes += pl.dx.partial_bytes;
   if (d->db != nullptr) {
-    pl.slices = std::max<int64_t>(1, std::min(d->rows / 128, 4 * kSms / ceil_div(d->out, 256)));
+    pl.slices = std::max<int64_t>(1, std::min(d->rows / 512, 8 * kSms / ceil_div(d->out, 64)));
     pl.db_at = pl.bytes;
     if (pl.slices > 1) pl.bytes += up(static_cast<size_t>(pl.slices) * d->out * 4);
   }
@@ -396,7 +451,10 @@ muon_status_t muon_linear(const muon_linear_t* d, void* workspace, size_t worksp
   e.add = epi_view(d->residual, d->rows, d->out);
   e.out = epi_view(d->y, d->rows, d->out);
   e.act = d->act;
-  st = run_product(pl.z, pl.x, false, pl.w, false, e, ws, pl.partial_at, false, &after, s);
+  ProductGroup g{};
+  g.first_blocks = small_blocks(pl.z);
+  if ((st = make_product(pl.z, pl.x, false, pl.w, false, e, ws, pl.partial_at, &after, &g.p[0])) != MUON_OK) return st;
+  st = run_product(pl.z, g, nullptr, s);
   if (st != MUON_OK || after.joins == 0) return st;
   after.begin[after.joins + 1] = after.begin[after.joins];
   return queued(launch_finish(after, s));
@@ -448,11 +506,12 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     t.cols = static_cast<int32_t>(d->out);
     t.accumulate = d->accumulate;
     t.slices = static_cast<int32_t>(pl.slices);
-    before.begin[before.packs + 1] += static_cast<int32_t>(ceil_div(d->out, 256) * pl.slices);
+    before.begin[before.packs + 1] += static_cast<int32_t>(ceil_div(d->out, 64) * pl.slices);
     after.sum = t;
   }
   if (before.begin[before.packs + 1] > 0)
     if ((st = queued(launch_prepare(before, s))) != MUON_OK) return st;
+  ProductGroup g{};
   if (dx) {
     Epilogue e{};
     e.rows = d->rows;
@@ -463,7 +522,9 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     }
     e.add = epi_view(d->skip, d->rows, d->in);
     e.out = epi_view(d->dx, d->rows, d->in);
-    st = run_product(pl.dx, pl.dy, false, pl.w, true, e, ws, pl.dx_at, false, &after, s);
+    st = make_product(pl.dx, pl.dy, false, pl.w, true, e, ws, pl.dx_at, &after, &g.p[0]);
+    g.first_blocks = small_blocks(pl.dx);
+    if (st == MUON_OK && !pl.dx.shared) st = run_product(pl.dx, g, nullptr, s);
     if (st != MUON_OK) return st;
   }
   if (dw) {
@@ -472,7 +533,11 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     e.cols = d->in;
     e.out = epi_view(d->dw, d->out, d->in);
     if (d->accumulate) e.add = e.out;
-    if ((st = run_product(pl.dw, pl.dy, true, pl.x, true, e, ws, pl.dw_at, dx, &after, s)) != MUON_OK) return st;
+    const int at = pl.dw.shared ? 1 : 0;
+    st = make_product(pl.dw, pl.dy, true, pl.x, true, e, ws, pl.dw_at, &after, &g.p[at]);
+    if (!pl.dw.shared) g.first_blocks = small_blocks(pl.dw);
+    if (st == MUON_OK) st = run_product(pl.dw, g, pl.dw.shared ? &pl.dw : nullptr, s);
+    if (st != MUON_OK) return st;
   }
   after.begin[after.joins + 1] = after.begin[after.joins];
   if (pl.slices > 1) after.begin[after.joins + 1] += static_cast<int32_t>(ceil_div(d->out, 32));

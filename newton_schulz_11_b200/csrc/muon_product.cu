@@ -74,19 +74,22 @@ __device__ __forceinline__ void tmem_store_row16(uint32_t taddr, const float* x)
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Per-CTA layout of a variant.  CG CTAs share a tile of 128 CG x TN; each stages its own 128
-// rows of A and TN / CG rows of B, 64 deep.
+// ------------------------------------------------------------------ large products
+//
+// A CTA pair shares a tile of 256 x 256 (tcgen05.mma.cta_group::2): each CTA stages its own
+// 128 rows of A and of B, 64 deep, 32 KB per k-block for 128 x 256 x 64 of work, in seven
+// stages; one thread of the leader CTA issues the MMAs; the two accumulators let the
+// epilogue of one tile run under the products of the next.  Persistent over a list of tiles.
 // SUM: the reduction in pieces added in registers.  FLIP: the tile's rows are the output's
 // columns.
-template <int CG_, int TN_, bool SUM_, bool FLIP_>
-struct Product {
-  static constexpr int CG = CG_, TM = 128 * CG_, TN = TN_, TNB = TN_ / CG_;
+template <bool SUM_, bool FLIP_>
+struct Pair {
+  static constexpr int TM = 256, TN = 256;
   static constexpr bool SUM = SUM_, FLIP = FLIP_;
   static constexpr int BK = kProductBK;
   static constexpr int kABytes = 128 * BK * 2;
-  static constexpr int kBBytes = TNB * BK * 2;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int S = (232448 - 1024 - 256) / kStageBytes < 10 ? (232448 - 1024 - 256) / kStageBytes : 10;
+  static constexpr int kStageBytes = 2 * kABytes;
+  static constexpr int S = 7;
   static constexpr int kBarOff = S * kStageBytes;
   static constexpr int kSmemBytes = kBarOff + 256 + 1024;
   // Epilogue warps.  (16, with half the columns each, measured 3-8% slower: 29.5 against
@@ -94,12 +97,11 @@ struct Product {
   static constexpr int NEPI = 8;
   static constexpr int kThreads = 64 + 32 * NEPI;
   static constexpr int NCW = TN * 4 / NEPI;       // accumulator columns per epilogue thread
-  static constexpr int NC = NCW < 32 ? NCW : 32;  // finished at a time
+  static constexpr int GC = 16;               // finished at a time; the common epilogue: 32
   static constexpr int kTmemCols = 2 * TN;
-  // whether the common epilogue can come up: a pair that sums has an fp32 output
-  static constexpr bool kPlain = !FLIP && !(SUM && CG == 2);
+  // whether the common epilogue can come up: a variant that sums has an fp32 output
+  static constexpr bool kPlain = !FLIP && !SUM;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
-  static_assert(kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
   static_assert((2 * S + 5) * 8 + 16 <= 256, "barrier area");
 };
 
@@ -126,24 +128,16 @@ __device__ __forceinline__ Unit decode_unit(const ProductParams& p, int t) {
   return u;
 }
 
-// One operand's k-block into `dst`: ROWS of its side from side0, 64 of k from k0.
-// K-major: one box of 64 k x ROWS.  Side-major (ROWS = 128): two boxes of 64 x 64 k.
-template <int CG, int ROWS>
-__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int mn, int side0, int k0,
-                                             uint64_t* bar, uint32_t bar_cluster) {
+// One operand's k-block into `dst`: 128 of its side from side0, 64 of k from k0, its bytes
+// completing on the leader's barrier.  K-major: one box of 64 k x 128; side-major: two boxes
+// of 64 x 64 k.
+__device__ __forceinline__ void load_pair_operand(uint8_t* dst, const CUtensorMap* map, int mn, int side0, int k0,
+                                                  uint32_t bar_cluster) {
   if (mn) {
-#pragma unroll
-    for (int b = 0; b < ROWS / 64; ++b) {
-      if constexpr (CG == 2)
-        tma_load_2d_pair(dst + b * 8192, map, bar_cluster, side0 + 64 * b, k0);
-      else
-        tma_load_2d(dst + b * 8192, map, bar, side0 + 64 * b, k0);
-    }
+    tma_load_2d_pair(dst, map, bar_cluster, side0, k0);
+    tma_load_2d_pair(dst + 8192, map, bar_cluster, side0 + 64, k0);
   } else {
-    if constexpr (CG == 2)
-      tma_load_2d_pair(dst, map, bar_cluster, k0, side0);
-    else
-      tma_load_2d(dst, map, bar, k0, side0);
+    tma_load_2d_pair(dst, map, bar_cluster, k0, side0);
   }
 }
 
@@ -168,8 +162,8 @@ __device__ __forceinline__ bool warp_waits(uint64_t* bar, uint32_t parity, const
 }
 
 template <class L>
-__global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __grid_constant__ ProductParams p) {
-  constexpr int CG = L::CG, S = L::S, TN = L::TN, NC = L::NC;
+__global__ void __launch_bounds__(L::kThreads, 1) muon_product_pair_kernel(const __grid_constant__ ProductParams p) {
+  constexpr int S = L::S, TN = L::TN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // used in the leader CTA
@@ -184,9 +178,9 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
-  const int worker = CG == 2 ? blockIdx.x >> 1 : blockIdx.x;
-  const int workers = CG == 2 ? gridDim.x >> 1 : gridDim.x;
+  const int rank = static_cast<int>(cluster_rank());
+  const int worker = blockIdx.x >> 1;
+  const int workers = gridDim.x >> 1;
   const int units = p.tiles_m * p.tiles_n * p.splits;
 
   if (threadIdx.x == 0) {
@@ -196,7 +190,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], CG * L::NEPI);
+      mbar_init(&tempty[a], 2 * L::NEPI);
     }
     mbar_init(tdown, 1);
     mbar_init(&pdone, 1);
@@ -208,27 +202,18 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
     tma_prefetch_desc(&p.map_b[0]);
   }
   if (warp == 1) {
-    if constexpr (CG == 2) {
-      tmem_alloc_pair(tmem_slot, L::kTmemCols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, L::kTmemCols);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(tmem_slot, L::kTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // the peer's barriers exist before anything arrives on them
+  cluster_sync();  // the peer's barriers exist before anything arrives on them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const Watchdog wd{abort_flag, g_layers_status, p.timeout_ns};
   // waits on the way out, for copies and MMAs in flight, end by themselves
   const unsigned long long tb = p.timeout_ns > 2000000000ull ? p.timeout_ns : 2000000000ull;
-  // Everything read or written below may belong to the launch before.  A product that runs
-  // beside the one before it (the two of a backward pass) depends on what came before that
-  // one only: its blocks start once all blocks of the other have passed this wait, so it
-  // need not wait here; it waits at its end, so that whatever follows finds both complete.
-  if (!p.beside) griddep_wait();
+  griddep_wait();  // everything read or written below may belong to the launch before
   griddep_launch_dependents();
 
   if (warp == 0) {
@@ -243,7 +228,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
       for (int t = worker; ok && t < units; t += workers) {
         const Unit u = decode_unit(p, t);
         const int a0 = L::TM * u.i + 128 * rank;
-        const int b0 = TN * u.j + L::TNB * rank;
+        const int b0 = TN * u.j + 128 * rank;
         for (int pb = u.kb0; ok && pb < u.kb1; pb += p.piece) {
           const int pe = pb + p.piece < u.kb1 ? pb + p.piece : u.kb1;
           for (int g = 0; ok && g < p.nseg; ++g) {
@@ -255,11 +240,11 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
                 break;
               }
               uint8_t* sa = smem + s * L::kStageBytes;
-              if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * L::kStageBytes);
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kStageBytes);
               const uint32_t fb = full0 + 8u * static_cast<uint32_t>(s);
               const int k0 = kb * L::BK;
-              load_operand<CG, 128>(sa, ma, p.a_mn, a0, k0, &full[s], fb);
-              load_operand<CG, L::TNB>(sa + L::kABytes, mb, p.b_mn, b0, k0, &full[s], fb);
+              load_pair_operand(sa, ma, p.a_mn, a0, k0, fb);
+              load_pair_operand(sa + L::kABytes, mb, p.b_mn, b0, k0, fb);
               ++issued;
               if (++s == S) {
                 s = 0;
@@ -279,13 +264,11 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
       } else {
         const uint32_t own = issued;
         uint32_t peer = own;
-        if constexpr (CG == 2) {
-          const uint64_t t0 = global_timer_ns();
-          bool known;
-          while (!(known = mbar_try_wait_cluster(&pdone, 0)) && global_timer_ns() - t0 < tb) {
-          }
-          if (known) peer = *peer_issued;
+        const uint64_t t0 = global_timer_ns();
+        bool known;
+        while (!(known = mbar_try_wait_cluster(&pdone, 0)) && global_timer_ns() - t0 < tb) {
         }
+        if (known) peer = *peer_issued;
         const uint32_t both = own < peer ? own : peer, most = own > peer ? own : peer;
         for (uint32_t i = both >= static_cast<uint32_t>(S) ? both - S : 0u; i < most; ++i) {
           uint64_t* bar = &full[i % S];
@@ -325,28 +308,17 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
               const uint32_t sa = smem_u32(smem + s * L::kStageBytes);
               const uint32_t sb = sa + L::kABytes;
 #pragma unroll
-              for (int kk = 0; kk < L::BK / 16; ++kk) {
-                if constexpr (CG == 2)
-                  umma_bf16_pair(dtm, slice_desc(sa, p.a_mn, kk), slice_desc(sb, p.b_mn, kk), idesc,
-                                 (kb | kk) != 0 ? 1u : 0u);
-                else
-                  umma_bf16(dtm, slice_desc(sa, p.a_mn, kk), slice_desc(sb, p.b_mn, kk), idesc,
-                            (kb | kk) != 0 ? 1u : 0u);
-              }
-              if constexpr (CG == 2)
-                umma_commit_pair(&empty[s], 0x3);
-              else
-                umma_commit(&empty[s]);
+              for (int kk = 0; kk < L::BK / 16; ++kk)
+                umma_bf16_pair(dtm, slice_desc(sa, p.a_mn, kk), slice_desc(sb, p.b_mn, kk), idesc,
+                               (kb | kk) != 0 ? 1u : 0u);
+              umma_commit_pair(&empty[s], 0x3);
               if (++s == S) {
                 s = 0;
                 ph ^= 1u;
               }
             }
             if (!ok) break;
-            if constexpr (CG == 2)
-              umma_commit_pair(&tfull[acc], 0x3);
-            else
-              umma_commit(&tfull[acc]);
+            umma_commit_pair(&tfull[acc], 0x3);
             if (++acc == 2) {
               acc = 0;
               aph ^= 1u;
@@ -354,10 +326,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
           }
         }
         // Every MMA has finished before either CTA releases tensor memory or leaves.
-        if constexpr (CG == 2)
-          umma_commit_pair(tdown, 0x3);
-        else
-          umma_commit(tdown);
+        umma_commit_pair(tdown, 0x3);
       }
       settle_wait(tdown, 0, tb);
     }
@@ -376,7 +345,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
       const int64_t row = static_cast<int64_t>(L::TM) * u.i + 128 * rank + r;
       const int64_t col = static_cast<int64_t>(TN) * u.j + h * L::NCW;
       float* part = p.partial == nullptr ? nullptr : p.partial + u.split * p.split_stride;
-      EpiRow<NC < 16 ? 16 : NC> at;
+      EpiRow<32> at;
       // the common epilogue, where all of the warp's rows and columns exist
       const bool plain =
           L::kPlain && p.e.plain && part == nullptr && row - lane + 32 <= p.e.rows && col + L::NCW <= p.e.cols;
@@ -439,51 +408,328 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_kernel(const __gr
         }
       }
       if (!ok) break;
+      if constexpr (L::kPlain) {
+        if (plain) {
 #pragma unroll 1
-      for (int c = 0; c < L::NCW; c += NC) {
-        uint32_t v[NC];
-        __syncwarp();  // lanes may have parted over edges
-        tmem_load_row<NC>(tacc + c, v);
-        if (c + NC == L::NCW) release();  // the last read
-        if (part != nullptr) {
-          float x[NC];
+          for (int c = 0; c < L::NCW; c += 32) {
+            uint32_t v[32];
+            tmem_load_row<32>(tacc + c, v);
+            if (c + 32 == L::NCW) release();  // the last read
+            F2 x[16];
 #pragma unroll
-          for (int j = 0; j < NC; ++j) x[j] = __uint_as_float(v[j]);
-          if constexpr (L::FLIP) {  // row: a feature; col: the first of NC tokens
-#pragma unroll
-            for (int j = 0; j < NC; ++j)
-              if (row < p.e.cols && col + c + j < p.e.rows) part[(col + c + j) * p.ld_partial + row] = x[j];
-          } else {
-            const EpiView out{part, p.ld_partial, 0, 2};
-            if (row < p.e.rows && col + c < p.ld_partial) store_segment<NC>(out, row * out.ld + col + c, NC, x);
+            for (int j = 0; j < 16; ++j) x[j] = pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            at.finish(p.e, col + c, c, c + 32 < L::NCW, x);
           }
           continue;
         }
-        F2 x[NC / 2];
+      }
+      // Everything else, in short steps: the code of a step has every choice in it, and a
+      // small product is over before a long one is in the instruction cache.
+      constexpr int GC = L::GC;
+#pragma unroll 1
+      for (int c = 0; c < L::NCW; c += GC) {
+        uint32_t v[GC];
+        __syncwarp();  // lanes may have parted over edges
+        tmem_load_row<GC>(tacc + c, v);
+        if (c + GC == L::NCW) release();  // the last read
+        if (part != nullptr) {
+          float x[GC];
 #pragma unroll
-        for (int j = 0; j < NC / 2; ++j) x[j] = pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-        if constexpr (L::FLIP) {
-          finish_column<NC>(p.e, col + c, row, x);
-        } else {
-          if (L::kPlain && plain)
-            at.finish(p.e, col + c, c, c + NC < L::NCW, x);
-          else
-            finish_segment<NC>(p.e, row, col + c, x);
+          for (int j = 0; j < GC; ++j) x[j] = __uint_as_float(v[j]);
+          if constexpr (L::FLIP) {  // row: a feature; col: the first of GC tokens
+#pragma unroll
+            for (int j = 0; j < GC; ++j)
+              if (row < p.e.cols && col + c + j < p.e.rows) part[(col + c + j) * p.ld_partial + row] = x[j];
+          } else {
+            const EpiView out{part, p.ld_partial, 0, 2};
+            if (row < p.e.rows && col + c < p.ld_partial) store_segment<GC>(out, row * out.ld + col + c, GC, x);
+          }
+          continue;
         }
+        F2 x[GC / 2];
+#pragma unroll
+        for (int j = 0; j < GC / 2; ++j) x[j] = pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        if constexpr (L::FLIP)
+          finish_column<GC>(p.e, col + c, row, x);
+        else
+          finish_segment<GC>(p.e, row, col + c, x);
       }
     }
   }
 
-  if (p.beside) griddep_wait();
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // nothing arrives on, or lands in, either CTA after this
+  cluster_sync();  // nothing arrives on, or lands in, either CTA after this
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (CG == 2)
-      tmem_dealloc_pair(tmem_base, L::kTmemCols);
-    else
-      tmem_dealloc(tmem_base, L::kTmemCols);
+    tmem_dealloc_pair(tmem_base, L::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ small products
+//
+// One tile of 128 x TN per cluster of 1, 2, 4 or 8 CTAs that split the reduction.  A small
+// product is bound by latency: by the few SMs its tiles would occupy (an SM takes in about
+// 64 bytes a cycle from L2: 12 k-blocks of 128 x 128 tiles take 5 us on one CTA), and by the
+// instructions of its epilogue.  The cluster divides both: each CTA sums its k-blocks in
+// tensor memory, leaves its tile in its own shared memory (the ring's, whose loads have all
+// been consumed), and finishes a share of the columns, adding the others' sums through
+// distributed shared memory in the order of the ranks.  No second launch, no workspace.
+// Two products of one call that both are small share a launch.
+template <int TN_, bool FLIP_>
+struct Small {
+  static constexpr int TN = TN_;
+  static constexpr bool FLIP = FLIP_;
+  static constexpr int BK = kProductBK;
+  static constexpr int kABytes = 128 * BK * 2;
+  static constexpr int kBBytes = TN * BK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int S = (232448 - 1280) / kStageBytes < 8 ? (232448 - 1280) / kStageBytes : 8;
+  static constexpr int kBarOff = S * kStageBytes;
+  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+  static constexpr int NEPI = 8;
+  static constexpr int kThreads = 64 + 32 * NEPI;
+  static constexpr int NCW = TN / 2;  // accumulator columns per epilogue thread
+  static constexpr int GC = 16;       // staged, and finished, at a time
+  static constexpr int kTmemCols = 2 * TN;
+  static_assert(128 * TN * 4 <= kBarOff, "the tile fits the ring");
+  static_assert((2 * S + 5) * 8 + 16 <= 256, "barrier area");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// As load_pair_operand, ROWS of the side, completing on this CTA's barrier.
+template <int ROWS>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int mn, int side0, int k0,
+                                             uint64_t* bar) {
+  if (mn) {
+#pragma unroll
+    for (int b = 0; b < ROWS / 64; ++b) tma_load_2d(dst + b * 8192, map, bar, side0 + 64 * b, k0);
+  } else {
+    tma_load_2d(dst, map, bar, k0, side0);
+  }
+}
+
+// A staged tile: 4 columns of a row in 16 bytes, the rows of a column group side by side, so
+// that a warp's 32 rows are conflict-free to write and to read.
+__device__ __forceinline__ uint32_t staged_at(int row, int col) {
+  return static_cast<uint32_t>(((col >> 2) * 128 + row) * 16);
+}
+
+template <class L>
+__global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(const __grid_constant__ ProductGroup g) {
+  constexpr int S = L::S, TN = L::TN, GC = L::GC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* tdown = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdown + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int second = static_cast<int>(blockIdx.x) >= g.first_blocks;
+  const ProductParams& p = g.p[second];
+  const int block = static_cast<int>(blockIdx.x) - (second ? g.first_blocks : 0);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int tile = block / p.splits;
+  const int j = tile / p.tiles_m, i = tile - j * p.tiles_m;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nk) * rank / p.splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nk) * (rank + 1) / p.splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], L::NEPI);
+    }
+    mbar_init(tdown, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.map_a[0]);
+    tma_prefetch_desc(&p.map_b[0]);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Watchdog wd{abort_flag, g_layers_status, p.timeout_ns};
+  const unsigned long long tb = p.timeout_ns > 2000000000ull ? p.timeout_ns : 2000000000ull;
+  griddep_wait();  // everything read or written below may belong to the launch before
+  griddep_launch_dependents();
+
+  // The share of the tile that this thread finishes: row r of the tile, 16 columns at a time.
+  const int e = static_cast<int>(threadIdx.x) - 64;
+  const int r = e & 127, q0 = rank + p.splits * (e >> 7);
+  const int64_t row = static_cast<int64_t>(128) * i + r;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, issued = 0;
+      bool ok = true;
+      for (int pb = kb0; ok && pb < kb1; pb += p.piece) {
+        const int pe = pb + p.piece < kb1 ? pb + p.piece : kb1;
+        for (int t = 0; ok && t < p.nseg; ++t) {
+          const CUtensorMap* ma = &p.map_a[p.seg_a[t]];
+          const CUtensorMap* mb = &p.map_b[p.seg_b[t]];
+          for (int kb = pb; kb < pe; ++kb) {
+            if (!mbar_wait(&empty[s], ph ^ 1u, wd, kSiteLoad)) {
+              ok = false;
+              break;
+            }
+            uint8_t* sa = smem + s * L::kStageBytes;
+            mbar_arrive_expect_tx(&full[s], L::kStageBytes);
+            load_operand<128>(sa, ma, p.a_mn, 128 * i, kb * L::BK, &full[s]);
+            load_operand<TN>(sa + L::kABytes, mb, p.b_mn, TN * j, kb * L::BK, &full[s]);
+            ++issued;
+            if (++s == S) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+      }
+      // every copy in flight has landed before anything else is put there
+      for (uint32_t l = issued >= static_cast<uint32_t>(S) ? issued - S : 0u; l < issued; ++l)
+        settle_wait(&full[l % S], (l / S) & 1u, tb);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(128, TN, p.a_mn, p.b_mn);
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int pb = kb0; ok && pb < kb1; pb += p.piece) {
+        const int pe = pb + p.piece < kb1 ? pb + p.piece : kb1;
+        const int blocks = (pe - pb) * p.nseg;
+        if (!mbar_wait(&tempty[acc], aph ^ 1u, wd, kSiteAccFree)) break;
+        tc_fence_after();
+        const uint32_t dtm = tmem_base + static_cast<uint32_t>(acc * TN);
+        for (int kb = 0; kb < blocks; ++kb) {
+          if (!mbar_wait(&full[s], ph, wd, kSiteStage)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * L::kStageBytes);
+          const uint32_t sb = sa + L::kABytes;
+#pragma unroll
+          for (int kk = 0; kk < L::BK / 16; ++kk)
+            umma_bf16(dtm, slice_desc(sa, p.a_mn, kk), slice_desc(sb, p.b_mn, kk), idesc, (kb | kk) != 0 ? 1u : 0u);
+          umma_commit(&empty[s]);
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&tfull[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1u;
+        }
+      }
+      umma_commit(tdown);
+      settle_wait(tdown, 0, tb);
+    }
+  } else {
+    // ---------------------------------------------------------------- sums, and the tile's staging
+    const int q4 = warp & 3;          // tensor memory lanes 32 q4 .. 32 q4 + 31 belong to this warp
+    const int c0 = ((warp - 2) >> 2) * L::NCW;
+    const int lane_row = q4 * 32 + lane;
+    if constexpr (!L::FLIP) {  // the epilogue's inputs move while the products run
+      const int64_t col = static_cast<int64_t>(TN) * j + GC * q0;
+      if (q0 < TN / GC && row < p.e.rows && col < p.e.cols) {
+        prefetch_row(p.e.slope, row, col, 1);
+        prefetch_row(p.e.add, row, col, 1);
+      }
+    }
+    float sum[L::NCW];
+#pragma unroll
+    for (int c = 0; c < L::NCW; ++c) sum[c] = 0.f;
+    int acc = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int pb = kb0; pb < kb1; pb += p.piece) {
+      ok = warp_waits(&tfull[acc], aph, wd, kSiteAccReady);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem_base + static_cast<uint32_t>(acc * TN + c0) + (static_cast<uint32_t>(q4 * 32) << 16);
+#pragma unroll
+      for (int c = 0; c < L::NCW; c += 16) {
+        uint32_t v[16];
+        tmem_load_row<16>(tacc + c, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sum[c + k] += __uint_as_float(v[k]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        aph ^= 1u;
+      }
+    }
+    if (ok) {  // the last accumulator is complete: every stage of the ring has been consumed
+#pragma unroll
+      for (int c = 0; c < L::NCW; c += 4)
+        *reinterpret_cast<float4*>(smem + staged_at(lane_row, c0 + c)) =
+            make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+    }
+  }
+
+  __syncwarp();
+  cluster_sync();  // every CTA's tile is staged
+  if (warp >= 2 && !*abort_flag) {
+#pragma unroll 1
+    for (int q = q0; q < TN / GC; q += 2 * p.splits) {
+      F2 v[GC / 2];
+#pragma unroll
+      for (int k = 0; k < GC / 2; ++k) v[k] = 0ull;  // zeros
+      for (int c = 0; c < p.splits; ++c) {
+        const uint32_t base = map_to_rank(smem_u32(smem), static_cast<uint32_t>(c)) + staged_at(r, GC * q);
+#pragma unroll
+        for (int k = 0; k < GC / 4; ++k) {
+          const float4 a = ld_cluster_f4(base + k * 2048u);
+          v[2 * k] = add2(v[2 * k], pair(a.x, a.y));
+          v[2 * k + 1] = add2(v[2 * k + 1], pair(a.z, a.w));
+        }
+      }
+      const int64_t col = static_cast<int64_t>(TN) * j + GC * q;
+      if constexpr (L::FLIP)  // row: a column of the output; col: the first of 16 of its rows
+        finish_column<GC>(p.e, col, row, v);
+      else
+        finish_segment<GC>(p.e, row, col, v);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // nobody reads this CTA's tile any more
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, L::kTmemCols);
   }
 }
 
@@ -525,17 +771,17 @@ __device__ __forceinline__ void pack_group(const PackTask& p, int64_t r, int g) 
   }
 }
 
-// Sums of columns over the rows: block b takes 256 columns, 8 a thread, and every slices-th
-// group of 8 rows.
-__device__ __forceinline__ void column_sums(const ColumnSumTask& p, int b, float (*red)[256]) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int blocks = (p.cols + 255) / 256;
-  const int slice = b / blocks, c0 = (b - slice * blocks) * 256;
-  const int c = c0 + lane * 8;
+// Sums of columns over the rows: block b takes 64 columns, 8 a thread, and every slices-th
+// group of 32 rows.
+__device__ __forceinline__ void column_sums(const ColumnSumTask& p, int b, float (*red)[64]) {
+  const int g = threadIdx.x & 7, w = threadIdx.x >> 3;
+  const int blocks = (p.cols + 63) / 64;
+  const int slice = b / blocks, c0 = (b - slice * blocks) * 64;
+  const int c = c0 + g * 8;
   F2 s[4] = {0ull, 0ull, 0ull, 0ull};  // zeros
   if (c < p.cols) {
 #pragma unroll 4
-    for (int64_t r = slice * 8 + w; r < p.rows; r += int64_t(8) * p.slices) {
+    for (int64_t r = slice * 32 + w; r < p.rows; r += int64_t(32) * p.slices) {
       F2 x[4];
       load_pairs<8>(p.src, r * p.src.ld + c, p.cols - c, x);
 #pragma unroll
@@ -543,12 +789,13 @@ __device__ __forceinline__ void column_sums(const ColumnSumTask& p, int b, float
     }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&red[w][lane * 8 + 2 * j]) = split(s[j]);
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&red[w][g * 8 + 2 * j]) = split(s[j]);
   __syncthreads();
   const int o = c0 + threadIdx.x;
-  if (o < p.cols) {
+  if (threadIdx.x < 64 && o < p.cols) {
     float t = red[0][threadIdx.x];
-    for (int k = 1; k < 8; ++k) t += red[k][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) t += red[k][threadIdx.x];
     if (p.slices == 1)
       p.out[o] = p.accumulate ? p.out[o] + t : t;
     else
@@ -557,7 +804,7 @@ __device__ __forceinline__ void column_sums(const ColumnSumTask& p, int b, float
 }
 
 __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant__ PrepareParams p) {
-  __shared__ float red[8][256];
+  __shared__ float red[32][64];
   griddep_wait();
   griddep_launch_dependents();
   int i = 0;
@@ -576,7 +823,7 @@ __device__ __forceinline__ void join_group(const JoinTask& p, int64_t m, int g) 
   const int64_t n = static_cast<int64_t>(g) * 8;
   const float* src = p.partial + m * p.ld_partial + n;
   F2 v[4] = {0ull, 0ull, 0ull, 0ull};  // zeros
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < p.splits; ++s) {
     const float4 a = *reinterpret_cast<const float4*>(src + s * p.split_stride);
     const float4 b = *reinterpret_cast<const float4*>(src + s * p.split_stride + 4);
@@ -623,52 +870,68 @@ __global__ void __launch_bounds__(256) muon_finish_kernel(const __grid_constant_
 // ------------------------------------------------------------------ launches
 
 template <class L>
-static cudaError_t launch_tiles(const ProductParams& p, int sms, cudaStream_t stream) {
-  auto* kernel = muon_product_kernel<L>;
+static cudaError_t launch_pair(const ProductParams& p, int sms, cudaStream_t stream) {
+  auto* kernel = muon_product_pair_kernel<L>;
   static thread_local int configured_device = -1;
-  static thread_local int resident = 0;  // workers (CTAs or pairs) that can run at once
+  static thread_local int resident = 0;  // pairs that can run at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
-    resident = sms / L::CG;
-    if (L::CG == 2) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(sms / 2 * 2, 1, 1);
-      cfg.blockDim = dim3(L::kThreads, 1, 1);
-      cfg.dynamicSmemBytes = L::kSmemBytes;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim = {2, 1, 1};
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int clusters = 0;
-      e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
-      if (e != cudaSuccess) return e;
-      resident = clusters > 0 ? clusters : 1;
-    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms / 2 * 2, 1, 1);
+    cfg.blockDim = dim3(L::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = L::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    resident = clusters > 0 ? clusters : 1;
     configured_device = dev;
   }
   const int units = p.tiles_m * p.tiles_n * p.splits;
-  return launch_dependent(kernel, p, dim3(static_cast<unsigned>(L::CG * std::min(units, resident))), L::kThreads,
-                          stream, L::kSmemBytes, L::CG);
+  return launch_dependent(kernel, p, dim3(static_cast<unsigned>(2 * std::min(units, resident))), L::kThreads, stream,
+                          L::kSmemBytes, 2);
 }
 
-template <int TILE>
-using ProductOf = Product<kTileShapes[TILE].ctas, kTileShapes[TILE].n, kTileShapes[TILE].sum, kTileShapes[TILE].flip>;
+template <class L>
+static cudaError_t launch_small(const ProductGroup& g, int blocks, cudaStream_t stream) {
+  auto* kernel = muon_product_small_kernel<L>;
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  return launch_dependent(kernel, g, dim3(static_cast<unsigned>(blocks)), L::kThreads, stream, L::kSmemBytes,
+                          g.p[0].splits);
+}
 
-cudaError_t launch_product(int tile, const ProductParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_product_pair(int tile, const ProductParams& p, int sms, cudaStream_t stream) {
   switch (tile) {
-    case kPair256: return launch_tiles<ProductOf<kPair256>>(p, sms, stream);
-    case kPair256Sum: return launch_tiles<ProductOf<kPair256Sum>>(p, sms, stream);
-    case kOne128: return launch_tiles<ProductOf<kOne128>>(p, sms, stream);
-    case kFlipPair256: return launch_tiles<ProductOf<kFlipPair256>>(p, sms, stream);
-    case kFlipPair256Sum: return launch_tiles<ProductOf<kFlipPair256Sum>>(p, sms, stream);
-    case kFlip128: return launch_tiles<ProductOf<kFlip128>>(p, sms, stream);
-    case kFlip32: return launch_tiles<ProductOf<kFlip32>>(p, sms, stream);
-    case kFlip64: return launch_tiles<ProductOf<kFlip64>>(p, sms, stream);
+    case kPair256: return launch_pair<Pair<false, false>>(p, sms, stream);
+    case kPair256Sum: return launch_pair<Pair<true, false>>(p, sms, stream);
+    case kFlipPair256: return launch_pair<Pair<false, true>>(p, sms, stream);
+    case kFlipPair256Sum: return launch_pair<Pair<true, true>>(p, sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_product_small(int tile, const ProductGroup& g, int blocks, cudaStream_t stream) {
+  switch (tile) {
+    case kOne128: return launch_small<Small<128, false>>(g, blocks, stream);
+    case kFlip128: return launch_small<Small<128, true>>(g, blocks, stream);
+    case kFlip32: return launch_small<Small<32, true>>(g, blocks, stream);
+    case kFlip64: return launch_small<Small<64, true>>(g, blocks, stream);
     default: return cudaErrorInvalidValue;
   }
 }

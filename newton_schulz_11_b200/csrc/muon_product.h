@@ -38,23 +38,23 @@ constexpr int kProductBK = 64;           // reduction depth of a k-block
 enum ProductTile : int {
   kPair256 = 0,     // 256 x 256 on a CTA pair, the whole reduction in tensor memory
   kPair256Sum,      // the same, the reduction in pieces that are added in registers
-  kOne128,          // 128 x 128 on one CTA, in pieces
-  kFlipPair256,     // as the first three
+  kFlipPair256,
   kFlipPair256Sum,
+  kOne128,          // 128 x 128 per cluster, in pieces (the small products, see muon_product.cu)
   kFlip128,
-  kFlip32,          // 128 columns x 32 tokens on one CTA, in pieces
+  kFlip32,          // 128 columns x 32 tokens
   kFlip64,          // 128 columns x 64 tokens
 };
 
 struct TileShape {
-  int m, n;    // rows and columns of the tile
-  int ctas;
-  bool flip, sum;
+  int m, n;  // rows and columns of the tile
+  bool pair, flip, sum;
 };
 
 constexpr TileShape kTileShapes[] = {
-    {256, 256, 2, false, false}, {256, 256, 2, false, true}, {128, 128, 1, false, true}, {256, 256, 2, true, false},
-    {256, 256, 2, true, true},   {128, 128, 1, true, true},  {128, 32, 1, true, true},   {128, 64, 1, true, true},
+    {256, 256, true, false, false}, {256, 256, true, false, true}, {256, 256, true, true, false},
+    {256, 256, true, true, true},   {128, 128, false, false, true}, {128, 128, false, true, true},
+    {128, 32, false, true, true},   {128, 64, false, true, true},
 };
 
 struct ProductParams {
@@ -64,20 +64,27 @@ struct ProductParams {
   int32_t a_mn, b_mn;         // majorness: 0 = contiguous along k, 1 = along the side
   int32_t tiles_m, tiles_n;
   int32_t nk;                 // k-blocks of the whole reduction
-  int32_t splits, kb_per_split;
+  int32_t splits;             // small products: CTAs of a cluster
+  int32_t kb_per_split;       // large products
   int32_t piece;              // k-blocks per piece
   int32_t nseg;
   uint8_t seg_a[8], seg_b[8]; // the terms of each segment, smallest products first
-  float* partial;             // [splits][e.rows][ld_partial] for the join kernel, or nullptr
+  float* partial;             // large products: [splits][e.rows][ld_partial] for the end, or nullptr
   int64_t ld_partial, split_stride;
-  int32_t beside;             // runs beside the product launched before it (see the kernel)
   unsigned long long timeout_ns;
+};
+
+// One launch of small products: the second, if any, from block first_blocks on.
+struct ProductGroup {
+  ProductParams p[2];
+  int32_t first_blocks;
 };
 
 // bf16 operand map of a matrix with rows of ld elements: boxes of 64 columns x box_rows rows.
 bool encode_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 
-cudaError_t launch_product(int tile, const ProductParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_product_pair(int tile, const ProductParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_product_small(int tile, const ProductGroup& g, int blocks, cudaStream_t stream);
 
 // How 256-thread blocks cover rows x groups of 8 columns: 2^shift threads along a row.
 struct Sweep {
