@@ -122,12 +122,16 @@ double pair_cost(const TileShape& shape, int64_t tiles, int64_t splits, int64_t 
   return splits == 1 ? cost : cost + 5500.0 + static_cast<double>((splits + 1) * outputs) * 4.0 / 2600.0;
 }
 
-//   a small product has its launch's start and its epilogue, which the cluster divides
+// Clusters of small products that run at the same time (what the occupancy calculator says).
+int64_t clusters_at_once(int64_t size) { return size == 1 ? kSms : size == 2 ? 74 : size == 4 ? 33 : 15; }
+
+//   a small product has its launch's start, its epilogue, which the cluster divides, and the
+//   cluster's two barriers
 double small_cost(const TileShape& shape, int64_t tiles, int64_t cluster, int64_t nk, int nseg) {
-  const double waves = static_cast<double>(ceil_div(tiles * cluster, kSms));
+  const double waves = static_cast<double>(ceil_div(tiles, clusters_at_once(cluster)));
   const double block = shape.n == 128 ? 760.0 : 700.0;
   return waves * (static_cast<double>(ceil_div(nk, cluster)) * block * nseg + 2500.0 + 30.0 * shape.n / cluster) +
-         (cluster > 1 ? 1000.0 : 0.0);
+         (cluster > 1 ? 2500.0 : 0.0);
 }
 
 // Picks the tile and the number of splits with the least estimated time.
@@ -148,7 +152,7 @@ Plan search_plan(int64_t m, int64_t n, int64_t k, const PlanTraits& t) {
       // (partial sums are aligned whatever the output is)
       const bool flip = !t.aligned && (!shape.pair || want == 1);
       if (!few && shape.flip != flip) continue;
-      if (shape.pair ? (ceil_div(best.nk, per) != want || (want > 1 && per < 2)) : want > best.nk) continue;
+      if (shape.pair && (ceil_div(best.nk, per) != want || (want > 1 && per < 2))) continue;
       const double cost = shape.pair ? pair_cost(shape, tm * tn, want, per, m * n, t.nseg)
                                      : small_cost(shape, tm * tn, want, best.nk, t.nseg);
       if (cost < best.cost) {
@@ -177,7 +181,7 @@ void share_launch(Plan* a, int64_t am, int64_t an, Plan* b, int64_t bm, int64_t 
   const int64_t btm = ceil_div(aligned ? bm : bn, 128), btn = ceil_div(aligned ? bn : bm, 128);
   double least = a->cost + b->cost + 3000.0;
   for (int64_t c = 1; c <= 8; c *= 2) {
-    if (c > std::min(a->nk, b->nk) || (atm * atn + btm * btn) * c > kSms) break;
+    if (atm * atn + btm * btn > clusters_at_once(c)) break;
     const double cost = std::max(small_cost(shape, atm * atn, c, a->nk, a->nseg),
                                  small_cost(shape, btm * btn, c, b->nk, b->nseg));
     if (cost >= least) continue;

@@ -351,10 +351,15 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_pair_kernel(const
           L::kPlain && p.e.plain && part == nullptr && row - lane + 32 <= p.e.rows && col + L::NCW <= p.e.cols;
       if constexpr (!L::FLIP) {  // the epilogue's inputs move while the tile's products run
         if (plain) at.start(p.e, row, col);
-        if (part == nullptr && row < p.e.rows && col < p.e.cols) {
-          const int width = p.e.cols - col < L::NCW ? static_cast<int>(p.e.cols - col) : L::NCW;
-          prefetch_row(p.e.slope, row, col, width);
-          prefetch_row(p.e.add, row, col, width);
+        if (part == nullptr && t + workers < units) {  // the next tile's inputs, a tile ahead
+          const Unit nx = decode_unit(p, t + workers);
+          const int64_t nrow = static_cast<int64_t>(L::TM) * nx.i + 128 * rank + r;
+          const int64_t ncol = static_cast<int64_t>(TN) * nx.j + h * L::NCW;
+          if (nrow < p.e.rows && ncol < p.e.cols) {
+            const int width = p.e.cols - ncol < L::NCW ? static_cast<int>(p.e.cols - ncol) : L::NCW;
+            prefetch_row(p.e.slope, nrow, ncol, width);
+            prefetch_row(p.e.add, nrow, ncol, width);
+          }
         }
         if constexpr (L::kPlain && !L::SUM) {
           if (plain) at.fetch(0);
@@ -490,7 +495,7 @@ struct Small {
   static constexpr int NEPI = 8;
   static constexpr int kThreads = 64 + 32 * NEPI;
   static constexpr int NCW = TN / 2;  // accumulator columns per epilogue thread
-  static constexpr int GC = 16;       // staged, and finished, at a time
+  static constexpr int GC = TN < 128 ? 8 : 16;  // finished at a time
   static constexpr int kTmemCols = 2 * TN;
   static_assert(128 * TN * 4 <= kBarOff, "the tile fits the ring");
   static_assert((2 * S + 5) * 8 + 16 <= 256, "barrier area");
@@ -544,8 +549,9 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
   const int rank = static_cast<int>(cluster_rank());
   const int tile = block / p.splits;
   const int j = tile / p.tiles_m, i = tile - j * p.tiles_m;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nk) * rank / p.splits);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nk) * (rank + 1) / p.splits);
+  // k-blocks of this CTA; of `parts` CTAs that have any (the others help with the epilogue)
+  const int per = (p.nk + p.splits - 1) / p.splits, parts = (p.nk + per - 1) / per;
+  const int kb0 = min(per * rank, p.nk), kb1 = min(kb0 + per, p.nk);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -692,7 +698,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
         aph ^= 1u;
       }
     }
-    if (ok) {  // the last accumulator is complete: every stage of the ring has been consumed
+    if (ok && kb0 < kb1) {  // the last accumulator is complete: every stage of the ring has been consumed
 #pragma unroll
       for (int c = 0; c < L::NCW; c += 4)
         *reinterpret_cast<float4*>(smem + staged_at(lane_row, c0 + c)) =
@@ -708,14 +714,25 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
       F2 v[GC / 2];
 #pragma unroll
       for (int k = 0; k < GC / 2; ++k) v[k] = 0ull;  // zeros
-      for (int c = 0; c < p.splits; ++c) {
-        const uint32_t base = map_to_rank(smem_u32(smem), static_cast<uint32_t>(c)) + staged_at(r, GC * q);
+#pragma unroll 1
+      for (int c = 0; c < parts; c += 2) {  // two CTAs' sums on their way at once
+        float4 a[2][GC / 4];
 #pragma unroll
-        for (int k = 0; k < GC / 4; ++k) {
-          const float4 a = ld_cluster_f4(base + k * 2048u);
-          v[2 * k] = add2(v[2 * k], pair(a.x, a.y));
-          v[2 * k + 1] = add2(v[2 * k + 1], pair(a.z, a.w));
-        }
+        for (int k = 0; k < 2; ++k)
+          if (c + k < parts) {
+            const uint32_t base = map_to_rank(smem_u32(smem), static_cast<uint32_t>(c + k)) + staged_at(r, GC * q);
+#pragma unroll
+            for (int l = 0; l < GC / 4; ++l) a[k][l] = ld_cluster_f4(base + l * 2048u);
+          }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (c + k < parts) {
+#pragma unroll
+            for (int l = 0; l < GC / 4; ++l) {
+              v[2 * l] = add2(v[2 * l], pair(a[k][l].x, a[k][l].y));
+              v[2 * l + 1] = add2(v[2 * l + 1], pair(a[k][l].z, a[k][l].w));
+            }
+          }
       }
       const int64_t col = static_cast<int64_t>(TN) * j + GC * q;
       if constexpr (L::FLIP)  // row: a column of the output; col: the first of 16 of its rows
