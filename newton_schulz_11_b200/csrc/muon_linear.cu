@@ -260,6 +260,7 @@ muon_status_t make_product(const Plan& pl, const Operand& a, bool a_mn, const Op
   const TileShape& shape = kTileShapes[pl.tile];
   const bool flip = shape.flip;
   const Operand &am = flip ? b : a, &bm = flip ? a : b;
+  *out = ProductParams{};
   ProductParams& p = *out;
   p.a_mn = flip ? b_mn : a_mn;
   p.b_mn = flip ? a_mn : b_mn;
@@ -300,7 +301,7 @@ muon_status_t make_product(const Plan& pl, const Operand& a, bool a_mn, const Op
 int small_blocks(const Plan& pl) { return static_cast<int>(pl.tiles_m * pl.tiles_n * pl.splits); }
 
 // Launches p (already made), or two small products that share a launch.
-muon_status_t run_product(const Plan& pl, const ProductGroup& g, const Plan* second, cudaStream_t s) {
+muon_status_t run_product(const Plan& pl, ProductGroup& g, const Plan* second, cudaStream_t s) {
   if (kTileShapes[pl.tile].pair) return queued(launch_product_pair(pl.tile, g.p[0], kSms, s));
   const int blocks = g.first_blocks + (second == nullptr ? 0 : small_blocks(*second));
   return queued(launch_product_small(pl.tile, g, blocks, s));
@@ -339,8 +340,26 @@ struct LinearGradPlan {
   Operand dy, x, w;
   Plan dx, dw;
   int64_t slices = 0;
+  int sum_blocks = 0;  // of the last product's launch that sum columns; 0: in the first launch
   size_t dx_at = 0, dw_at = 0, db_at = 0, bytes = 0;
 };
+
+// How many blocks that would be idle under the call's last product can sum the columns of dy
+// in less time than that product takes, or 0.  A block takes 256 rows of 64 columns in about
+// a microsecond (eight loads in flight a thread), a product 0.4 us a k-block.
+int idle_blocks(const Plan& last, const Plan& other, int64_t tasks, int64_t rows) {
+  const int size = kTileShapes[last.tile].pair ? 2 : static_cast<int>(last.splits);
+  int64_t used = last.tiles_m * last.tiles_n * (kTileShapes[last.tile].pair ? 2 * last.splits : last.splits);
+  if (last.shared) used += other.tiles_m * other.tiles_n * other.splits;
+  int64_t idle = (kSms - used) / size * size;
+  if (size > 2) idle = std::min<int64_t>(idle, clusters_at_once(size) * size - used);
+  idle = std::min(idle, ceil_div(tasks, size) * size);
+  if (idle <= 0) return 0;
+  const double sums = static_cast<double>(ceil_div(tasks, idle)) * (static_cast<double>(rows) / 256.0 + 2.0);
+  const double product = 4.0 + 0.4 * last.nseg * (kTileShapes[last.tile].pair ? last.kb_per_split
+                                                                              : ceil_div(last.nk, last.splits));
+  return sums <= product ? static_cast<int>(idle) : 0;
+}
 
 LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
   LinearGradPlan pl;
@@ -369,11 +388,21 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
   pl.dx_at = pl.bytes;
   pl.bytes += pl.dx.partial_bytes;
   if (d->db != nullptr) {
-    pl.slices = std::max<int64_t>(1, std::min(d->rows / 512, 8 * kSms / ceil_div(d->out, 64)));
+    const int64_t tasks = ceil_div(d->out, 64);
+    pl.sum_blocks = dx || dw ? idle_blocks(dw ? pl.dw : pl.dx, pl.dx, tasks, d->rows) : 0;
+    pl.slices = pl.sum_blocks > 0 ? 1 : std::max<int64_t>(1, std::min(d->rows / 512, 8 * kSms / tasks));
     pl.db_at = pl.bytes;
     if (pl.slices > 1) pl.bytes += up(static_cast<size_t>(pl.slices) * d->out * 4);
   }
   return pl;
+}
+
+// Lets the last product's launch sum the columns, where the plan says so.
+void add_sums(const LinearGradPlan& pl, int64_t cols, const ColumnSumTask& sum, ProductGroup* g) {
+  if (pl.sum_blocks == 0) return;
+  g->p[0].sum = sum;
+  g->p[0].sum_tasks = static_cast<int32_t>(ceil_div(cols, 64));
+  g->p[0].sum_blocks = pl.sum_blocks;
 }
 
 muon_status_t take_workspace(Operands* ops, void* ws, size_t have, size_t need) {
@@ -510,7 +539,7 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     t.cols = static_cast<int32_t>(d->out);
     t.accumulate = d->accumulate;
     t.slices = static_cast<int32_t>(pl.slices);
-    before.begin[before.packs + 1] += static_cast<int32_t>(ceil_div(d->out, 64) * pl.slices);
+    if (pl.sum_blocks == 0) before.begin[before.packs + 1] += static_cast<int32_t>(ceil_div(d->out, 64) * pl.slices);
     after.sum = t;
   }
   if (before.begin[before.packs + 1] > 0)
@@ -528,6 +557,7 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     e.out = epi_view(d->dx, d->rows, d->in);
     st = make_product(pl.dx, pl.dy, false, pl.w, true, e, ws, pl.dx_at, &after, &g.p[0]);
     g.first_blocks = small_blocks(pl.dx);
+    if (!dw) add_sums(pl, d->out, after.sum, &g);
     if (st == MUON_OK && !pl.dx.shared) st = run_product(pl.dx, g, nullptr, s);
     if (st != MUON_OK) return st;
   }
@@ -540,6 +570,7 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     const int at = pl.dw.shared ? 1 : 0;
     st = make_product(pl.dw, pl.dy, true, pl.x, true, e, ws, pl.dw_at, &after, &g.p[at]);
     if (!pl.dw.shared) g.first_blocks = small_blocks(pl.dw);
+    add_sums(pl, d->out, after.sum, &g);
     if (st == MUON_OK) st = run_product(pl.dw, g, pl.dw.shared ? &pl.dw : nullptr, s);
     if (st != MUON_OK) return st;
   }

@@ -74,6 +74,49 @@ __device__ __forceinline__ void tmem_store_row16(uint32_t taddr, const float* x)
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Sums of columns over the rows: block b takes 64 columns, 8 a thread, and every slices-th
+// group of 32 rows.  256 threads.
+__device__ __forceinline__ void column_sums(const ColumnSumTask& p, int b, float (*red)[64]) {
+  const int g = threadIdx.x & 7, w = threadIdx.x >> 3;
+  const int blocks = (p.cols + 63) / 64;
+  const int slice = b / blocks, c0 = (b - slice * blocks) * 64;
+  const int c = c0 + g * 8;
+  F2 s[4] = {0ull, 0ull, 0ull, 0ull};  // zeros
+  if (c < p.cols) {
+#pragma unroll 8
+    for (int64_t r = slice * 32 + w; r < p.rows; r += int64_t(32) * p.slices) {
+      F2 x[4];
+      load_pairs<8>(p.src, r * p.src.ld + c, p.cols - c, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] = add2(s[j], x[j]);
+    }
+  }
+  named_barrier(1, 256);  // an earlier task's sums have been read
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&red[w][g * 8 + 2 * j]) = split(s[j]);
+  named_barrier(1, 256);
+  const int o = c0 + threadIdx.x;
+  if (threadIdx.x < 64 && o < p.cols) {
+    float t = red[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) t += red[k][threadIdx.x];
+    if (p.slices == 1)
+      p.out[o] = p.accumulate ? p.out[o] + t : t;
+    else
+      p.partial[static_cast<int64_t>(slice) * p.cols + o] = t;
+  }
+}
+
+// The blocks of a product's launch that sum columns instead.
+__device__ __forceinline__ void run_column_sums(const ProductParams& p, uint8_t* smem) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (threadIdx.x >= 256) return;
+  float(*red)[64] = reinterpret_cast<float(*)[64]>(smem);
+  for (int b = static_cast<int>(blockIdx.x) - p.sum_from; b < p.sum_tasks; b += p.sum_blocks)
+    column_sums(p.sum, b, red);
+}
+
 // ------------------------------------------------------------------ large products
 //
 // A CTA pair shares a tile of 256 x 256 (tcgen05.mma.cta_group::2): each CTA stages its own
@@ -180,8 +223,9 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_pair_kernel(const
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
   const int worker = blockIdx.x >> 1;
-  const int workers = gridDim.x >> 1;
+  const int workers = p.sum_from >> 1;
   const int units = p.tiles_m * p.tiles_n * p.splits;
+  if (static_cast<int>(blockIdx.x) >= p.sum_from) return run_column_sums(p, smem);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -541,6 +585,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdown + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  if (static_cast<int>(blockIdx.x) >= g.p[0].sum_from) return run_column_sums(g.p[0], smem);
   const int second = static_cast<int>(blockIdx.x) >= g.first_blocks;
   const ProductParams& p = g.p[second];
   const int block = static_cast<int>(blockIdx.x) - (second ? g.first_blocks : 0);
@@ -788,38 +833,6 @@ __device__ __forceinline__ void pack_group(const PackTask& p, int64_t r, int g) 
   }
 }
 
-// Sums of columns over the rows: block b takes 64 columns, 8 a thread, and every slices-th
-// group of 32 rows.
-__device__ __forceinline__ void column_sums(const ColumnSumTask& p, int b, float (*red)[64]) {
-  const int g = threadIdx.x & 7, w = threadIdx.x >> 3;
-  const int blocks = (p.cols + 63) / 64;
-  const int slice = b / blocks, c0 = (b - slice * blocks) * 64;
-  const int c = c0 + g * 8;
-  F2 s[4] = {0ull, 0ull, 0ull, 0ull};  // zeros
-  if (c < p.cols) {
-#pragma unroll 4
-    for (int64_t r = slice * 32 + w; r < p.rows; r += int64_t(32) * p.slices) {
-      F2 x[4];
-      load_pairs<8>(p.src, r * p.src.ld + c, p.cols - c, x);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] = add2(s[j], x[j]);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&red[w][g * 8 + 2 * j]) = split(s[j]);
-  __syncthreads();
-  const int o = c0 + threadIdx.x;
-  if (threadIdx.x < 64 && o < p.cols) {
-    float t = red[0][threadIdx.x];
-#pragma unroll
-    for (int k = 1; k < 32; ++k) t += red[k][threadIdx.x];
-    if (p.slices == 1)
-      p.out[o] = p.accumulate ? p.out[o] + t : t;
-    else
-      p.partial[static_cast<int64_t>(slice) * p.cols + o] = t;
-  }
-}
-
 __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant__ PrepareParams p) {
   __shared__ float red[32][64];
   griddep_wait();
@@ -887,7 +900,7 @@ __global__ void __launch_bounds__(256) muon_finish_kernel(const __grid_constant_
 // ------------------------------------------------------------------ launches
 
 template <class L>
-static cudaError_t launch_pair(const ProductParams& p, int sms, cudaStream_t stream) {
+static cudaError_t launch_pair(ProductParams& p, int sms, cudaStream_t stream) {
   auto* kernel = muon_product_pair_kernel<L>;
   static thread_local int configured_device = -1;
   static thread_local int resident = 0;  // pairs that can run at once
@@ -912,13 +925,13 @@ static cudaError_t launch_pair(const ProductParams& p, int sms, cudaStream_t str
     resident = clusters > 0 ? clusters : 1;
     configured_device = dev;
   }
-  const int units = p.tiles_m * p.tiles_n * p.splits;
-  return launch_dependent(kernel, p, dim3(static_cast<unsigned>(2 * std::min(units, resident))), L::kThreads, stream,
+  p.sum_from = 2 * std::min(p.tiles_m * p.tiles_n * p.splits, resident);
+  return launch_dependent(kernel, p, dim3(static_cast<unsigned>(p.sum_from + p.sum_blocks)), L::kThreads, stream,
                           L::kSmemBytes, 2);
 }
 
 template <class L>
-static cudaError_t launch_small(const ProductGroup& g, int blocks, cudaStream_t stream) {
+static cudaError_t launch_small(ProductGroup& g, int blocks, cudaStream_t stream) {
   auto* kernel = muon_product_small_kernel<L>;
   static thread_local int configured_device = -1;
   int dev = 0;
@@ -929,11 +942,12 @@ static cudaError_t launch_small(const ProductGroup& g, int blocks, cudaStream_t 
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  return launch_dependent(kernel, g, dim3(static_cast<unsigned>(blocks)), L::kThreads, stream, L::kSmemBytes,
-                          g.p[0].splits);
+  g.p[0].sum_from = blocks;
+  return launch_dependent(kernel, g, dim3(static_cast<unsigned>(blocks + g.p[0].sum_blocks)), L::kThreads, stream,
+                          L::kSmemBytes, g.p[0].splits);
 }
 
-cudaError_t launch_product_pair(int tile, const ProductParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_product_pair(int tile, ProductParams& p, int sms, cudaStream_t stream) {
   switch (tile) {
     case kPair256: return launch_pair<Pair<false, false>>(p, sms, stream);
     case kPair256Sum: return launch_pair<Pair<true, false>>(p, sms, stream);
@@ -943,7 +957,7 @@ cudaError_t launch_product_pair(int tile, const ProductParams& p, int sms, cudaS
   }
 }
 
-cudaError_t launch_product_small(int tile, const ProductGroup& g, int blocks, cudaStream_t stream) {
+cudaError_t launch_product_small(int tile, ProductGroup& g, int blocks, cudaStream_t stream) {
   switch (tile) {
     case kOne128: return launch_small<Small<128, false>>(g, blocks, stream);
     case kFlip128: return launch_small<Small<128, true>>(g, blocks, stream);

@@ -57,6 +57,15 @@ constexpr TileShape kTileShapes[] = {
     {128, 32, false, true, true},   {128, 64, false, true, true},
 };
 
+// Column sums of a matrix, in `slices` partial sums over its rows.
+struct ColumnSumTask {
+  EpiView src;
+  float* out;
+  float* partial;  // [slices][cols]
+  int64_t rows;
+  int32_t cols, accumulate, slices;
+};
+
 struct ProductParams {
   CUtensorMap map_a[kTerms];  // operand on the tile's M side
   CUtensorMap map_b[kTerms];  // operand on the tile's N side
@@ -72,6 +81,10 @@ struct ProductParams {
   float* partial;             // large products: [splits][e.rows][ld_partial] for the end, or nullptr
   int64_t ld_partial, split_stride;
   unsigned long long timeout_ns;
+  // The bias gradient rides along where the products leave SMs idle: blocks from sum_from on
+  // (a whole number of clusters) run its sum_tasks instead.
+  ColumnSumTask sum;
+  int32_t sum_from, sum_tasks, sum_blocks;
 };
 
 // One launch of small products: the second, if any, from block first_blocks on.
@@ -83,8 +96,8 @@ struct ProductGroup {
 // bf16 operand map of a matrix with rows of ld elements: boxes of 64 columns x box_rows rows.
 bool encode_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 
-cudaError_t launch_product_pair(int tile, const ProductParams& p, int sms, cudaStream_t stream);
-cudaError_t launch_product_small(int tile, const ProductGroup& g, int blocks, cudaStream_t stream);
+cudaError_t launch_product_pair(int tile, ProductParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_product_small(int tile, ProductGroup& g, int blocks, cudaStream_t stream);
 
 // How 256-thread blocks cover rows x groups of 8 columns: 2^shift threads along a row.
 struct Sweep {
@@ -112,15 +125,6 @@ struct PackTask {
   int64_t ld_dst, term_stride;
   int32_t cols, terms;
   Sweep sweep;
-};
-
-// Column sums of a matrix, in `slices` partial sums over its rows.
-struct ColumnSumTask {
-  EpiView src;
-  float* out;
-  float* partial;  // [slices][cols]
-  int64_t rows;
-  int32_t cols, accumulate, slices;
 };
 
 // What precedes the products of a call, in one launch: blocks [begin[i], begin[i + 1]) run

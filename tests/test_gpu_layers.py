@@ -314,6 +314,71 @@ def test_linear_backward(rows, n_in, n_out, xt, wt, yt):
         close(db, rdb, e_b + 2 * U * (np.abs(rdb) + np.abs(f64(db0))), "db")
 
 
+# Sizes that the plan runs as CTA pairs, with and without a split reduction, and as small
+# products together and apart; the odd ones leave output rows off 16 bytes.
+LARGE_SIZES = [(256, 256, 8192), (4096, 256, 512), (2304, 768, 768), (1500, 2048, 2560), (1501, 2049, 1283),
+               (40, 4096, 6000), (9000, 256, 264), (128, 5000, 128), (3, 3123, 4422)]
+
+
+def tol64(a, b, k):
+    return (k / 16 + 16) * 2.0 ** -23 * (a.abs() @ b.abs().t()) + 1e-38
+
+
+def close64(got, want, tol, what):
+    off = (got.double() - want).abs() - tol
+    assert got.shape == want.shape and not torch.isnan(off).any(), what
+    assert (off <= 0).all(), f"{what}: {int((off > 0).sum())} of {off.numel()} off, by up to {float(off.max()):.3e}"
+
+
+@pytest.mark.parametrize("xt,wt,yt,act", [("bf16", "bf16", "bf16", "gelu"), ("bf16", "bf16", "f32", "silu"),
+                                          ("f32", "f32", "f32", "relu2"), ("bf16", "f32", "bf16", "gelu_tanh")])
+@pytest.mark.parametrize("rows,n_in,n_out", LARGE_SIZES)
+def test_linear_large(rows, n_in, n_out, xt, wt, yt, act):
+    """As test_linear and test_linear_backward, with the fp64 products taken on the GPU."""
+    require_gpu()
+    from newton_schulz_11_b200 import api
+
+    gen = torch.Generator(device="cuda").manual_seed(rows + n_in + n_out)
+
+    def mk(r, c, dt, std):
+        return (torch.randn(r, c, generator=gen, device="cuda") * std).to(DT[dt])
+
+    on = lambda f, t, *a: torch.from_numpy(f(f64(t), *a)).cuda()  # noqa: E731
+    half = HALF[DT[yt]]
+    x, w, bias, res = mk(rows, n_in, xt, 1.0), mk(n_out, n_in, wt, n_in ** -0.5), mk(1, n_out, wt, 0.5)[0], mk(
+        rows, n_out, yt, 1.0)
+    y, z = torch.empty(rows, n_out, device="cuda", dtype=DT[yt]), torch.empty(rows, n_out, device="cuda", dtype=DT[yt])
+    api.linear(x, w, bias, act=act, residual=res, out=y, preact=z)
+    rz = x.double() @ w.double().t() + bias.double()
+    e_z = tol64(x.double(), w.double(), n_in) + 2 * U * (rz.abs() + bias.double().abs())
+    close64(z, rz, e_z + half * rz.abs(), "z")
+    ry = on(lo.act, rz, act) + res.double()
+    lip = 2 * rz.abs() + 1e-3 if act == "relu2" else 1.13
+    e_y = lip * e_z + e_z * e_z + torch.from_numpy(act_error(f64(rz), act)).cuda()
+    close64(y, ry, e_y + 2 * U * (ry.abs() + res.double().abs()) + half * ry.abs(), "y")
+
+    dy, zin, skip = mk(rows, n_out, xt, 0.1), mk(rows, n_in, xt, 1.0), mk(rows, n_in, yt, 0.1)
+    dw0 = torch.randn(n_out, n_in, generator=gen, device="cuda")
+    db0 = torch.randn(n_out, generator=gen, device="cuda")
+    dw, db, dx = dw0.clone(), db0.clone(), torch.empty(rows, n_in, device="cuda", dtype=DT[yt])
+    api.linear_backward(dy, x, w, in_act=act, in_preact=zin, skip=skip, dx=dx, dw=dw, db=db, accumulate=True)
+    g = dy.double()
+    plain = g @ w.double()
+    slope = on(lo.act_slope, zin, act)
+    rdx = plain * slope + skip.double()
+    e_x = tol64(g, w.double().t(), n_out) * slope.abs() + plain.abs() * 2.0 ** -19 * (1 + slope.abs())
+    close64(dx, rdx, e_x + 2 * U * (rdx.abs() + skip.double().abs()) + half * rdx.abs() + 1e-38, "dx")
+    rdw = g.t() @ x.double() + dw0.double()
+    close64(dw, rdw, tol64(g.t(), x.double().t(), rows) + 2 * U * (rdw.abs() + dw0.double().abs()), "dw")
+    rdb = g.sum(0) + db0.double()
+    close64(db, rdb, (rows / 2 + 40) * U * g.abs().sum(0) + 2 * U * (rdb.abs() + db0.double().abs()), "db")
+    # each gradient by itself is the same
+    only = api.linear_backward(dy, x, w, need_dx=False, need_dw=False)[2]
+    close64(only, g.sum(0), (rows / 2 + 40) * U * g.abs().sum(0) + 1e-38, "db alone")
+    only = api.linear_backward(dy, x, w, need_dx=False, need_db=False)[1]
+    close64(only, g.t() @ x.double(), tol64(g.t(), x.double().t(), rows), "dw alone")
+
+
 @pytest.mark.parametrize("rows,n_in,n_out", [(200, 64, 200), (300, 4096, 136), (4096, 264, 136), (5, 2048, 64)])
 def test_fp32_products_hold_fp32(rows, n_in, n_out):
     """fp32 operands and fp32 results: the Frobenius error stays at a few fp32 steps.
