@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "muon_epilogue.cuh"
 #include "muon_layers_host.h"
@@ -22,11 +23,12 @@ namespace muon {
 struct ActGradParams {
   EpiView dy, z, dz;
   Sweep sweep;
-  int32_t cols, act;
+  int32_t cols, act, wide;
 };
 
-// Eight columns of a row per thread and step.
-__global__ void __launch_bounds__(256, 6) muon_activation_backward_kernel(const __grid_constant__ ActGradParams p) {
+// Eight columns of a row per thread and step; in whole rows of 16-column groups (p.wide) 16,
+// 32 bytes of each bf16 operand at a time.
+__global__ void __launch_bounds__(256, 5) muon_activation_backward_kernel(const __grid_constant__ ActGradParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const Sweep& s = p.sweep;
@@ -36,12 +38,31 @@ __global__ void __launch_bounds__(256, 6) muon_activation_backward_kernel(const 
   for (int64_t r = static_cast<int64_t>(rb) * deep + (threadIdx.x >> s.shift); r < s.rows;
        r += static_cast<int64_t>(s.row_blocks) * deep)
     for (int gr = g0; gr < s.groups; gr += s.col_blocks << s.shift) {
-      const int c = gr * 8, valid = p.cols - c;
-      F2 g[4], z[4];
-      load_pairs<8>(p.dy, r * p.dy.ld + c, valid, g);
-      load_pairs<8>(p.z, r * p.z.ld + c, valid, z);
-      apply_slope<4>(p.act, z, g);
-      store_pairs<8>(p.dz, r * p.dz.ld + c, valid, g);
+      if (p.wide) {
+        const int c = gr * 16;
+        const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(p.dy.p) + r * p.dy.ld + c;
+        const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(p.z.p) + r * p.z.ld + c;
+        uint4 a, b, e, f;
+        ld_global_v8(dy, a, b);
+        ld_global_v8(z, e, f);
+        const uint32_t gw[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint32_t zw[8] = {e.x, e.y, e.z, e.w, f.x, f.y, f.z, f.w};
+        F2 g[8], t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          g[j] = EpiRow<16>::value(gw[j]);
+          t[j] = EpiRow<16>::value(zw[j]);
+        }
+        apply_slope<8>(p.act, t, g);
+        EpiRow<16>::store(reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(p.dz.p) + r * p.dz.ld + c), g);
+      } else {
+        const int c = gr * 8, valid = p.cols - c;
+        F2 g[4], z[4];
+        load_pairs<8>(p.dy, r * p.dy.ld + c, valid, g);
+        load_pairs<8>(p.z, r * p.z.ld + c, valid, z);
+        apply_slope<4>(p.act, z, g);
+        store_pairs<8>(p.dz, r * p.dz.ld + c, valid, g);
+      }
     }
 }
 
@@ -596,7 +617,10 @@ muon_status_t muon_activation_backward(const muon_activation_grad_t* d, void* st
   p.dy = epi_view(d->dy, d->rows, d->cols);
   p.z = epi_view(d->z, d->rows, d->cols);
   p.dz = epi_view(d->dz, d->rows, d->cols);
-  p.sweep = make_sweep(d->rows, ceil_div(d->cols, 8), 12 * kSms);
+  p.wide = d->cols % 16 == 0;
+  for (const EpiView* v : {&p.dy, &p.z, &p.dz})
+    if (!v->bf16 || v->vec != 2) p.wide = 0;
+  p.sweep = make_sweep(d->rows, ceil_div(d->cols, p.wide ? 16 : 8), 12 * kSms);
   p.cols = static_cast<int32_t>(d->cols);
   p.act = d->act;
   return queued(launch_dependent(muon_activation_backward_kernel, p,

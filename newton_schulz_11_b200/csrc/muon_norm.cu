@@ -54,17 +54,19 @@ struct NormGradParams {
 // kernels are bound by instruction issue before memory (in scalar form the backward pass
 // took 37 instructions an element, and 209 us instead of 149 us at 32768 x 4096).
 
-template <int TPR_, int NV_, bool BF16_, bool VEC_>
+enum Form : int { kLoose = 0, kGroups8 = 1, kFull = 2 };  // not VEC; VEC; VEC and no thread without columns
+
+template <int TPR_, int NV_, bool BF16_, int FORM_>
 struct Rows {
   static constexpr int TPR = TPR_, NV = NV_;
-  static constexpr bool BF16 = BF16_, VEC = VEC_;
+  static constexpr bool BF16 = BF16_, VEC = FORM_ != kLoose, FULL = FORM_ == kFull;
   static constexpr int kThreads = TPR == 32 ? 128 : TPR;
   static constexpr int kGroups = kThreads / TPR;  // rows in flight per block
   static constexpr int kWarps = TPR / 32;         // warps per row
   // blocks per SM: what the registers allow, so that the persistent grid is one wave
   static constexpr int kForward = TPR == 32 ? (NV == 1 ? 8 : NV == 2 ? 6 : 4) : TPR == 128 ? 6 : TPR == 256 && NV == 2 ? 3
                                   : TPR == 256 ? 2 : 1;
-  static constexpr int kBackward = TPR == 32 ? (NV == 1 ? 5 : NV == 2 ? 4 : 3) : TPR == 128 ? 4
+  static constexpr int kBackward = TPR == 32 ? (NV == 1 ? 6 : NV <= 3 ? 4 : 3) : TPR == 128 ? 4
                                    : TPR == 256 && NV == 2 ? 2 : 1;
 };
 
@@ -72,6 +74,12 @@ struct Rows {
 template <class L>
 __device__ __forceinline__ int column(int v, int j, int t) {
   return L::VEC ? (v * L::TPR + t) * 8 + j : (v * 8 + j) * L::TPR + t;
+}
+
+// Whether column c of this thread exists.
+template <class L>
+__device__ __forceinline__ bool exists(int c, int cols) {
+  return L::FULL || c < cols;
 }
 
 // Group k of a vector (a gain, a bias), zero past the last column.
@@ -97,7 +105,7 @@ template <class L, bool BF16>
 __device__ __forceinline__ void store_group(const EpiView& v, int64_t off, int k, int t, int cols, const F2 (&x)[4]) {
   if constexpr (L::VEC) {
     const int c = column<L>(k, 0, t);
-    if (c >= cols) return;
+    if (!exists<L>(c, cols)) return;
     const float2 a = split(x[0]), b = split(x[1]), d = split(x[2]), e = split(x[3]);
     if constexpr (BF16) {
       const __nv_bfloat162 q[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(b.x, b.y),
@@ -223,12 +231,12 @@ __device__ __forceinline__ void staged_group(const uint8_t* row, int bf16, int k
     const int c = column<L>(k, 0, t);
     uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
     if (bf16) {
-      if (c < cols) a = *reinterpret_cast<const uint4*>(row + 2 * c);
+      if (exists<L>(c, cols)) a = *reinterpret_cast<const uint4*>(row + 2 * c);
       const uint32_t q[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = pair(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xFFFF0000u));
     } else {
-      if (c < cols) {
+      if (exists<L>(c, cols)) {
         a = *reinterpret_cast<const uint4*>(row + 4 * c);
         b = *reinterpret_cast<const uint4*>(row + 4 * c + 16);
       }
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kForward) muon_layer_norm_ring
 #pragma unroll
     for (int k = 0; k < L::NV; ++k) {
       if constexpr (L::VEC) {
-        if (column<L>(k, 0, t) < p.cols) {
+        if (exists<L>(column<L>(k, 0, t), p.cols)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             x[k][j] = add2(x[k][j], shift);
@@ -604,31 +612,29 @@ __global__ void __launch_bounds__(256) muon_layer_norm_columns_kernel(const __gr
 
 // ------------------------------------------------------------------ parameter gradients
 
-// Adds the slices' partial sums: 32 columns per block, 16 warps over the slices.
-__global__ void __launch_bounds__(512) muon_layer_norm_join_kernel(const __grid_constant__ NormGradParams p) {
-  __shared__ float sum[16][2][32];
+// Adds the slices' partial sums: 32 columns of one gradient per block, 32 warps over the
+// slices with eight loads each on their way (a few hundred slices, so a few latencies).
+__global__ void __launch_bounds__(1024) muon_layer_norm_join_kernel(const __grid_constant__ NormGradParams p) {
+  __shared__ float sum[32][33];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, which = blockIdx.y;
   const int c = blockIdx.x * 32 + lane;
-  float dg = 0.f, db = 0.f;
+  float* out = which == 0 ? p.dgain : p.dbias;
+  if (out == nullptr) return;
+  float t = 0.f;
   if (c < p.cols) {
-#pragma unroll 4
-    for (int s = w; s < p.slices; s += 16) {
-      const float* o = p.partial + static_cast<int64_t>(s) * 2 * p.cols;
-      dg += o[c];
-      db += o[p.cols + c];
-    }
+    const float* o = p.partial + static_cast<int64_t>(which) * p.cols + c;
+#pragma unroll 8
+    for (int s = w; s < p.slices; s += 32) t += o[static_cast<int64_t>(s) * 2 * p.cols];
   }
-  sum[w][0][lane] = dg;
-  sum[w][1][lane] = db;
+  sum[w][lane] = t;
   __syncthreads();
-  if (w < 2 && c < p.cols) {
-    float t = 0.f;
+  if (w == 0 && c < p.cols) {
+    t = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) t += sum[k][w][lane];
-    float* out = w == 0 ? p.dgain : p.dbias;
-    if (out != nullptr) out[c] = p.accumulate ? out[c] + t : t;
+    for (int k = 0; k < 32; ++k) t += sum[k][lane];
+    out[c] = p.accumulate ? out[c] + t : t;
   }
 }
 
@@ -704,7 +710,7 @@ muon_status_t launch_rows(const P& p, int64_t blocks, int threads, int smem, cud
   return queued(launch_dependent(Kernel, p, dim3(static_cast<unsigned>(blocks)), threads, s, smem));
 }
 
-template <int T, int N, bool BF16, bool VEC>
+template <int T, int N, bool BF16, int VEC>
 muon_status_t run_norm(NormParams p, cudaStream_t s) {
   using L = Rows<T, N, BF16, VEC>;
   const RingSize ring = ring_size(slot_bytes(p.cols * (BF16 ? 2 : 4)), L::kGroups, L::kForward, 0);
@@ -716,11 +722,11 @@ muon_status_t run_norm(NormParams p, cudaStream_t s) {
 // Row blocks of the backward pass, each with a partial sum of its own.
 template <int T, int N>
 int64_t grad_blocks(int64_t rows) {
-  using L = Rows<T, N, true, true>;
+  using L = Rows<T, N, true, kFull>;
   return row_blocks(rows, L::kGroups, L::kBackward);
 }
 
-template <int T, int N, bool BF16, bool VEC>
+template <int T, int N, bool BF16, int VEC>
 muon_status_t run_norm_grad(NormGradParams p, cudaStream_t s) {
   using L = Rows<T, N, BF16, VEC>;
   const int64_t stage = 2 * slot_bytes(p.cols * (BF16 ? 2 : 4)) +
@@ -780,8 +786,16 @@ extern "C" muon_status_t muon_layer_norm(const muon_layer_norm_t* d, void* strea
                                    dim3(static_cast<unsigned>(row_blocks(d->rows, 1, 4))), kWideThreads, s));
   const bool vec = whole_groups(d->cols, {&p.x, &p.y, &p.gain, &p.bias}), bf16 = p.x.bf16 != 0;
   return with_shape(d->cols, [&](auto t, auto n) {
-    if (vec) return bf16 ? run_norm<t(), n(), true, true>(p, s) : run_norm<t(), n(), false, true>(p, s);
-    return bf16 ? run_norm<t(), n(), true, false>(p, s) : run_norm<t(), n(), false, false>(p, s);
+    // Forward, the checks for missing columns cost instructions where a warp or a wide block
+    // has the row, and help where they happen to space its accesses (us, with and without, at
+    // 134 M elements or 32768 rows): bf16 768 19.4, 18.2; 2048 50, 53; 4096 91, 100; 8192 110,
+    // 107; fp32 1024 51, 54; 4096 100, 95.  (Backward they always cost: 4096 bf16 149, 131.)
+    constexpr bool wide32 = t() >= 128, full16 = t() == 32 || t() == 512;
+    const bool full = d->cols == t() * n() * 8;
+    if (vec && full && bf16 && full16) return run_norm<t(), n(), true, full16 ? kFull : kGroups8>(p, s);
+    if (vec && full && !bf16 && wide32) return run_norm<t(), n(), false, wide32 ? kFull : kGroups8>(p, s);
+    if (vec) return bf16 ? run_norm<t(), n(), true, kGroups8>(p, s) : run_norm<t(), n(), false, kGroups8>(p, s);
+    return bf16 ? run_norm<t(), n(), true, kLoose>(p, s) : run_norm<t(), n(), false, kLoose>(p, s);
   });
 }
 
@@ -856,11 +870,15 @@ extern "C" muon_status_t muon_layer_norm_backward(const muon_layer_norm_grad_t* 
   } else {
     const bool vec = whole_groups(d->cols, {&p.x, &p.dy, &p.gain, &p.skip, &p.dx}), bf16 = p.x.bf16 != 0;
     st = with_shape(d->cols, [&](auto t, auto n) {
-      if (vec) return bf16 ? run_norm_grad<t(), n(), true, true>(p, s) : run_norm_grad<t(), n(), false, true>(p, s);
-      return bf16 ? run_norm_grad<t(), n(), true, false>(p, s) : run_norm_grad<t(), n(), false, false>(p, s);
+      const bool full = d->cols == t() * n() * 8;
+      if (vec && full)
+        return bf16 ? run_norm_grad<t(), n(), true, kFull>(p, s) : run_norm_grad<t(), n(), false, kFull>(p, s);
+      if (vec)
+        return bf16 ? run_norm_grad<t(), n(), true, kGroups8>(p, s) : run_norm_grad<t(), n(), false, kGroups8>(p, s);
+      return bf16 ? run_norm_grad<t(), n(), true, kLoose>(p, s) : run_norm_grad<t(), n(), false, kLoose>(p, s);
     });
   }
   if (st != MUON_OK || !grads) return st;
-  return queued(launch_dependent(muon_layer_norm_join_kernel, p, dim3(static_cast<unsigned>(ceil_div(d->cols, 32))),
-                                 512, s));
+  return queued(launch_dependent(muon_layer_norm_join_kernel, p, dim3(static_cast<unsigned>(ceil_div(d->cols, 32)), 2),
+                                 1024, s));
 }

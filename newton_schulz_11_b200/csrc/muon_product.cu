@@ -871,7 +871,7 @@ __device__ __forceinline__ void join_column_sums(const ColumnSumTask& p, int b, 
   const int c = b * 32 + lane;
   float t = 0.f;
   if (c < p.cols) {
-#pragma unroll 4
+#pragma unroll 8
     for (int s = w; s < p.slices; s += 8) t += p.partial[static_cast<int64_t>(s) * p.cols + c];
   }
   red[w][lane] = t;
