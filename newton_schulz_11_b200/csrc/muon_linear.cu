@@ -146,12 +146,13 @@ double pair_cost(const TileShape& shape, int64_t tiles, int64_t splits, int64_t 
 // Clusters of small products that run at the same time (what the occupancy calculator says).
 int64_t clusters_at_once(int64_t size) { return size == 1 ? kSms : size == 2 ? 74 : size == 4 ? 33 : 15; }
 
-//   a small product has its launch's start, its epilogue, which the cluster divides, and the
-//   cluster's two barriers
+//   a small product loads each term of a k-block once; it has its launch's start, its epilogue,
+//   which the cluster divides, and the cluster's two barriers
 double small_cost(const TileShape& shape, int64_t tiles, int64_t cluster, int64_t nk, int nseg) {
   const double waves = static_cast<double>(ceil_div(tiles, clusters_at_once(cluster)));
   const double block = shape.n == 128 ? 760.0 : 700.0;
-  return waves * (static_cast<double>(ceil_div(nk, cluster)) * block * nseg + 2500.0 + 30.0 * shape.n / cluster) +
+  const double loads = nseg == 1 ? 1.0 : nseg == kTerms ? 2.0 : 3.0;  // of a bf16 product's
+  return waves * (static_cast<double>(ceil_div(nk, cluster)) * block * loads + 2500.0 + 30.0 * shape.n / cluster) +
          (cluster > 1 ? 2500.0 : 0.0);
 }
 
@@ -201,21 +202,24 @@ void share_launch(Plan* a, int64_t am, int64_t an, Plan* b, int64_t bm, int64_t 
   const int64_t atm = ceil_div(aligned ? am : an, 128), atn = ceil_div(aligned ? an : am, 128);
   const int64_t btm = ceil_div(aligned ? bm : bn, 128), btn = ceil_div(aligned ? bn : bm, 128);
   double least = a->cost + b->cost + 3000.0;
-  for (int64_t c = 1; c <= 8; c *= 2) {
-    if (atm * atn + btm * btn > clusters_at_once(c)) break;
-    const double cost = std::max(small_cost(shape, atm * atn, c, a->nk, a->nseg),
-                                 small_cost(shape, btm * btn, c, b->nk, b->nseg));
-    if (cost >= least) continue;
-    least = cost;
-    a->shared = b->shared = true;
-    a->tile = b->tile = tile;
-    a->splits = b->splits = c;
-    a->tiles_m = atm;
-    a->tiles_n = atn;
-    b->tiles_m = btm;
-    b->tiles_n = btn;
-    a->partial_bytes = b->partial_bytes = 0;
-  }
+  for (int64_t ca = 1; ca <= 8; ca *= 2)
+    for (int64_t cb = 1; cb <= 8; cb *= 2) {  // a cluster holds several tiles of the product that is split less
+      const int64_t c = std::max(ca, cb);
+      if (ceil_div(atm * atn * ca, c) + ceil_div(btm * btn * cb, c) > clusters_at_once(c)) continue;
+      const double cost = std::max(small_cost(shape, atm * atn, ca, a->nk, a->nseg),
+                                   small_cost(shape, btm * btn, cb, b->nk, b->nseg));
+      if (cost >= least) continue;
+      least = cost;
+      a->shared = b->shared = true;
+      a->tile = b->tile = tile;
+      a->splits = ca;
+      b->splits = cb;
+      a->tiles_m = atm;
+      a->tiles_n = atn;
+      b->tiles_m = btm;
+      b->tiles_n = btn;
+      a->partial_bytes = b->partial_bytes = 0;
+    }
 }
 
 // The search takes a microsecond or two; a call asks for its plan twice (its workspace, then
@@ -297,6 +301,7 @@ muon_status_t make_product(const Plan& pl, const Operand& a, bool a_mn, const Op
   p.kb_per_split = static_cast<int32_t>(pl.kb_per_split);
   p.piece = shape.sum ? static_cast<int32_t>(kPieceBlocks) : p.kb_per_split;
   p.nseg = pl.nseg;
+  p.walk = am.terms == 1 ? (bm.terms == 1 ? kWalkOne : kWalkCols) : (bm.terms == 1 ? kWalkRows : kWalkBoth);
   for (int g = 0; g < pl.nseg; ++g) {  // the smallest products first
     p.seg_a[g] = static_cast<uint8_t>(am.terms == 1 ? 0 : bm.terms == 1 ? pl.nseg - 1 - g : both_a[g]);
     p.seg_b[g] = static_cast<uint8_t>(bm.terms == 1 ? 0 : am.terms == 1 ? pl.nseg - 1 - g : both_b[g]);
@@ -319,12 +324,17 @@ muon_status_t make_product(const Plan& pl, const Operand& a, bool a_mn, const Op
   return MUON_OK;
 }
 
-int small_blocks(const Plan& pl) { return static_cast<int>(pl.tiles_m * pl.tiles_n * pl.splits); }
+// Blocks of a small product in clusters of `cluster`.
+int small_blocks(const Plan& pl, int64_t cluster) {
+  return static_cast<int>(ceil_div(pl.tiles_m * pl.tiles_n * pl.splits, cluster) * cluster);
+}
 
 // Launches p (already made), or two small products that share a launch.
 muon_status_t run_product(const Plan& pl, ProductGroup& g, const Plan* second, cudaStream_t s) {
   if (kTileShapes[pl.tile].pair) return queued(launch_product_pair(pl.tile, g.p[0], kSms, s));
-  const int blocks = g.first_blocks + (second == nullptr ? 0 : small_blocks(*second));
+  g.cluster = static_cast<int32_t>(second == nullptr ? pl.splits : std::max(pl.splits, second->splits));
+  g.first_blocks = small_blocks(pl, g.cluster);
+  const int blocks = g.first_blocks + (second == nullptr ? 0 : small_blocks(*second, g.cluster));
   return queued(launch_product_small(pl.tile, g, blocks, s));
 }
 
@@ -369,16 +379,17 @@ struct LinearGradPlan {
 // in less time than that product takes, or 0.  A block takes 256 rows of 64 columns in about
 // a microsecond (eight loads in flight a thread), a product 0.4 us a k-block.
 int idle_blocks(const Plan& last, const Plan& other, int64_t tasks, int64_t rows) {
-  const int size = kTileShapes[last.tile].pair ? 2 : static_cast<int>(last.splits);
-  int64_t used = last.tiles_m * last.tiles_n * (kTileShapes[last.tile].pair ? 2 * last.splits : last.splits);
-  if (last.shared) used += other.tiles_m * other.tiles_n * other.splits;
+  const bool pair = kTileShapes[last.tile].pair;
+  const int size = pair ? 2 : static_cast<int>(last.shared ? std::max(last.splits, other.splits) : last.splits);
+  int64_t used = pair ? 2 * last.tiles_m * last.tiles_n * last.splits : small_blocks(last, size);
+  if (last.shared) used += small_blocks(other, size);
   int64_t idle = (kSms - used) / size * size;
   if (size > 2) idle = std::min<int64_t>(idle, clusters_at_once(size) * size - used);
   idle = std::min(idle, ceil_div(tasks, size) * size);
   if (idle <= 0) return 0;
   const double sums = static_cast<double>(ceil_div(tasks, idle)) * (static_cast<double>(rows) / 256.0 + 2.0);
-  const double product = 4.0 + 0.4 * last.nseg * (kTileShapes[last.tile].pair ? last.kb_per_split
-                                                                              : ceil_div(last.nk, last.splits));
+  const double product =
+      4.0 + 0.4 * (pair ? last.nseg * last.kb_per_split : (last.nseg + 1) / 2 * ceil_div(last.nk, last.splits));
   return sums <= product ? static_cast<int>(idle) : 0;
 }
 
@@ -506,7 +517,6 @@ muon_status_t muon_linear(const muon_linear_t* d, void* workspace, size_t worksp
   e.out = epi_view(d->y, d->rows, d->out);
   e.act = d->act;
   ProductGroup g{};
-  g.first_blocks = small_blocks(pl.z);
   if ((st = make_product(pl.z, pl.x, false, pl.w, false, e, ws, pl.partial_at, &after, &g.p[0])) != MUON_OK) return st;
   st = run_product(pl.z, g, nullptr, s);
   if (st != MUON_OK || after.joins == 0) return st;
@@ -577,7 +587,6 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     e.add = epi_view(d->skip, d->rows, d->in);
     e.out = epi_view(d->dx, d->rows, d->in);
     st = make_product(pl.dx, pl.dy, false, pl.w, true, e, ws, pl.dx_at, &after, &g.p[0]);
-    g.first_blocks = small_blocks(pl.dx);
     if (!dw) add_sums(pl, d->out, after.sum, &g);
     if (st == MUON_OK && !pl.dx.shared) st = run_product(pl.dx, g, nullptr, s);
     if (st != MUON_OK) return st;
@@ -590,9 +599,8 @@ muon_status_t muon_linear_backward(const muon_linear_grad_t* d, void* workspace,
     if (d->accumulate) e.add = e.out;
     const int at = pl.dw.shared ? 1 : 0;
     st = make_product(pl.dw, pl.dy, true, pl.x, true, e, ws, pl.dw_at, &after, &g.p[at]);
-    if (!pl.dw.shared) g.first_blocks = small_blocks(pl.dw);
     add_sums(pl, d->out, after.sum, &g);
-    if (st == MUON_OK) st = run_product(pl.dw, g, pl.dw.shared ? &pl.dw : nullptr, s);
+    if (st == MUON_OK) st = pl.dw.shared ? run_product(pl.dx, g, &pl.dw, s) : run_product(pl.dw, g, nullptr, s);
     if (st != MUON_OK) return st;
   }
   after.begin[after.joins + 1] = after.begin[after.joins];

@@ -532,17 +532,18 @@ struct Small {
   static constexpr int BK = kProductBK;
   static constexpr int kABytes = 128 * BK * 2;
   static constexpr int kBBytes = TN * BK * 2;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int S = (232448 - 1280) / kStageBytes < 8 ? (232448 - 1280) / kStageBytes : 8;
-  static constexpr int kBarOff = S * kStageBytes;
-  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+  static constexpr int S = 14;  // loads of one operand term that the ring holds
+  static constexpr int kBarOff = S * kABytes;
+  static constexpr int kPairs = kBarOff / (kABytes + kBBytes) < S ? kBarOff / (kABytes + kBBytes) : S;
+  static constexpr int kSmemBytes = kBarOff + 512 + 1024;
   static constexpr int NEPI = 8;
   static constexpr int kThreads = 64 + 32 * NEPI;
   static constexpr int NCW = TN / 2;  // accumulator columns per epilogue thread
   static constexpr int GC = TN < 128 ? 8 : 16;  // finished at a time
-  static constexpr int kTmemCols = 2 * TN;
+  static constexpr int kTmemCols = 4 * TN;
+  static_assert(kSmemBytes <= 232448, "shared memory of a block");
   static_assert(128 * TN * 4 <= kBarOff, "the tile fits the ring");
-  static_assert((2 * S + 5) * 8 + 16 <= 256, "barrier area");
+  static_assert((2 * S + 5) * 8 + 16 <= 512, "barrier area");
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -572,6 +573,139 @@ __device__ __forceinline__ uint32_t staged_at(int row, int col) {
   return static_cast<uint32_t>(((col >> 2) * 128 + row) * 16);
 }
 
+// The walk of a k-block: the operand terms in the order they are loaded (side 0: the tile's
+// rows; term 0 leading, 1 middle, 2 low), and the term products with the loads they use, wait
+// for and are the last to use.  Each term is loaded once a k-block (a walk per term product
+// would load 2 per product: 12, not 6), and the order frees them early.  The leading terms'
+// product has an accumulator of its own: beside it the others are corrections, 2^-8 and less
+// of its size, whose own truncation is nothing.
+struct WalkStep {
+  int a, b, need, correction, frees;  // frees: bit per load
+};
+template <int WALK>
+struct Walk;
+template <>
+struct Walk<kWalkOne> {
+  static constexpr int kLoads = 2, kSteps = 1, kRing = 0;  // a place holds both loads: Small::kPairs of them
+  int side[2] = {0, 1}, term[2] = {0, 0};
+  WalkStep step[1] = {{0, 1, 1, 0, 1}};
+};
+template <>
+struct Walk<kWalkRows> {
+  static constexpr int kLoads = 4, kSteps = 3, kRing = 12;
+  int side[4] = {0, 1, 0, 0}, term[4] = {2, 0, 1, 0};
+  WalkStep step[3] = {{0, 1, 2, 1, 1}, {2, 1, 3, 1, 4}, {3, 1, 4, 0, 2 + 8}};
+};
+template <>
+struct Walk<kWalkCols> {
+  static constexpr int kLoads = 4, kSteps = 3, kRing = 12;
+  int side[4] = {1, 0, 1, 1}, term[4] = {2, 0, 1, 0};
+  WalkStep step[3] = {{1, 0, 2, 1, 1}, {1, 2, 3, 1, 4}, {1, 3, 4, 0, 2 + 8}};
+};
+template <>
+struct Walk<kWalkBoth> {
+  static constexpr int kLoads = 6, kSteps = 6, kRing = 12;
+  int side[6] = {0, 1, 0, 1, 0, 1}, term[6] = {2, 0, 1, 1, 0, 2};
+  // l h, m h, m m, h h, h m, h l
+  WalkStep step[6] = {{0, 1, 2, 1, 1}, {2, 1, 3, 1, 0}, {2, 3, 4, 1, 4},
+                                      {4, 1, 5, 0, 2}, {4, 3, 5, 1, 8}, {4, 5, 6, 1, 16 + 32}};
+};
+
+struct SmallBars {
+  uint64_t *full, *empty, *tfull, *tempty;
+};
+
+// The producer's loads of k-blocks [kb0, kb1); `budget` bounds the last wait, for the copies
+// still in flight.
+template <class L, class W>
+__device__ __forceinline__ void small_loads(const ProductParams& p, uint8_t* smem, const SmallBars& bar,
+                                            const Watchdog& wd, int i, int j, int kb0, int kb1,
+                                            unsigned long long budget) {
+  constexpr W w{};
+  constexpr bool joint = W::kSteps == 1;
+  constexpr int kPlaces = joint ? L::kPairs : W::kRing, kPlace = joint ? L::kABytes + L::kBBytes : L::kABytes;
+  int s = 0;
+  uint32_t ph = 0, issued = 0;
+  bool ok = true;
+  for (int kb = kb0; ok && kb < kb1; ++kb) {
+#pragma unroll
+    for (int l = 0; l < W::kLoads; ++l) {
+      uint8_t* dst = smem + s * kPlace + l * L::kABytes;
+      uint64_t* full = &bar.full[joint ? s : s + l];
+      if (!joint || l == 0) {
+        ok = mbar_wait(&bar.empty[s + l], ph ^ 1u, wd, kSiteLoad);
+        if (!ok) break;
+        mbar_arrive_expect_tx(full, joint ? L::kABytes + L::kBBytes : w.side[l] == 0 ? L::kABytes : L::kBBytes);
+      }
+      if (w.side[l] == 0)
+        load_operand<128>(dst, &p.map_a[w.term[l]], p.a_mn, 128 * i, kb * L::BK, full);
+      else
+        load_operand<L::TN>(dst, &p.map_b[w.term[l]], p.b_mn, L::TN * j, kb * L::BK, full);
+      if (!joint || l == 0) ++issued;
+    }
+    if ((s += joint ? 1 : W::kLoads) == kPlaces) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+  // every copy in flight has landed before anything else is put there
+  for (uint32_t l = issued >= static_cast<uint32_t>(kPlaces) ? issued - kPlaces : 0u; l < issued; ++l)
+    settle_wait(&bar.full[l % kPlaces], (l / kPlaces) & 1u, budget);
+}
+
+// The MMA issuer's half.
+template <class L, class W>
+__device__ __forceinline__ void small_products(const ProductParams& p, uint8_t* smem, const SmallBars& bar,
+                                               const Watchdog& wd, uint32_t tmem_base, int kb0, int kb1) {
+  constexpr W w{};
+  constexpr int TN = L::TN;
+  constexpr bool joint = W::kSteps == 1;
+  constexpr int kPlaces = joint ? L::kPairs : W::kRing, kPlace = joint ? L::kABytes + L::kBBytes : L::kABytes;
+  const uint32_t idesc = idesc_bf16_f32(128, TN, p.a_mn, p.b_mn);
+  int s = 0, acc = 0;
+  uint32_t ph = 0, aph = 0;
+  for (int pb = kb0; pb < kb1; pb += p.piece) {
+    const int pe = pb + p.piece < kb1 ? pb + p.piece : kb1;
+    if (!mbar_wait(&bar.tempty[acc], aph ^ 1u, wd, kSiteAccFree)) return;
+    tc_fence_after();
+    const uint32_t dtm = tmem_base + static_cast<uint32_t>(2 * acc * TN);
+    for (int kb = pb; kb < pe; ++kb) {
+      const uint32_t base = smem_u32(smem + s * kPlace);
+      int there = 0, begun = 0;
+#pragma unroll
+      for (int t = 0; t < W::kSteps; ++t) {
+        const WalkStep step = w.step[t];
+#pragma unroll
+        for (int l = 0; l < W::kLoads; ++l)
+          if (l >= there && l < step.need)
+            if (!mbar_wait(&bar.full[s + l], ph, wd, kSiteStage)) return;
+        there = step.need;
+        tc_fence_after();
+        const uint32_t sa = base + step.a * L::kABytes, sb = base + step.b * L::kABytes;
+        const uint32_t d = dtm + static_cast<uint32_t>(step.correction * TN);
+        const bool later = begun >> step.correction & 1;
+#pragma unroll
+        for (int kk = 0; kk < L::BK / 16; ++kk)
+          umma_bf16(d, slice_desc(sa, p.a_mn, kk), slice_desc(sb, p.b_mn, kk), idesc,
+                    kk != 0 || later || kb != pb ? 1u : 0u);
+        begun |= 1 << step.correction;
+#pragma unroll
+        for (int l = 0; l < W::kLoads; ++l)
+          if (step.frees >> l & 1) umma_commit(&bar.empty[s + l]);
+      }
+      if ((s += joint ? 1 : W::kLoads) == kPlaces) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    umma_commit(&bar.tfull[acc]);
+    if (++acc == 2) {
+      acc = 0;
+      aph ^= 1u;
+    }
+  }
+}
+
 template <class L>
 __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(const __grid_constant__ ProductGroup g) {
   constexpr int S = L::S, TN = L::TN, GC = L::GC;
@@ -591,12 +725,15 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
   const int block = static_cast<int>(blockIdx.x) - (second ? g.first_blocks : 0);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank());
+  // the p.splits CTAs of a tile are neighbours in the cluster, from rank `first` on
+  const int in_cluster = static_cast<int>(cluster_rank());
+  const int rank = in_cluster & (p.splits - 1), first = in_cluster - rank;
   const int tile = block / p.splits;
   const int j = tile / p.tiles_m, i = tile - j * p.tiles_m;
+  const bool live = j < p.tiles_n;  // the last cluster may have CTAs left over
   // k-blocks of this CTA; of `parts` CTAs that have any (the others help with the epilogue)
   const int per = (p.nk + p.splits - 1) / p.splits, parts = (p.nk + per - 1) / per;
-  const int kb0 = min(per * rank, p.nk), kb1 = min(kb0 + per, p.nk);
+  const int kb0 = live ? min(per * rank, p.nk) : 0, kb1 = live ? min(kb0 + per, p.nk) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -624,6 +761,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const Watchdog wd{abort_flag, g_layers_status, p.timeout_ns};
+  const SmallBars bar{full, empty, tfull, tempty};
   const unsigned long long tb = p.timeout_ns > 2000000000ull ? p.timeout_ns : 2000000000ull;
   griddep_wait();  // everything read or written below may belong to the launch before
   griddep_launch_dependents();
@@ -636,71 +774,21 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0, issued = 0;
-      bool ok = true;
-      for (int pb = kb0; ok && pb < kb1; pb += p.piece) {
-        const int pe = pb + p.piece < kb1 ? pb + p.piece : kb1;
-        for (int t = 0; ok && t < p.nseg; ++t) {
-          const CUtensorMap* ma = &p.map_a[p.seg_a[t]];
-          const CUtensorMap* mb = &p.map_b[p.seg_b[t]];
-          for (int kb = pb; kb < pe; ++kb) {
-            if (!mbar_wait(&empty[s], ph ^ 1u, wd, kSiteLoad)) {
-              ok = false;
-              break;
-            }
-            uint8_t* sa = smem + s * L::kStageBytes;
-            mbar_arrive_expect_tx(&full[s], L::kStageBytes);
-            load_operand<128>(sa, ma, p.a_mn, 128 * i, kb * L::BK, &full[s]);
-            load_operand<TN>(sa + L::kABytes, mb, p.b_mn, TN * j, kb * L::BK, &full[s]);
-            ++issued;
-            if (++s == S) {
-              s = 0;
-              ph ^= 1u;
-            }
-          }
-        }
+      switch (p.walk) {
+        case kWalkOne: small_loads<L, Walk<kWalkOne>>(p, smem, bar, wd, i, j, kb0, kb1, tb); break;
+        case kWalkRows: small_loads<L, Walk<kWalkRows>>(p, smem, bar, wd, i, j, kb0, kb1, tb); break;
+        case kWalkCols: small_loads<L, Walk<kWalkCols>>(p, smem, bar, wd, i, j, kb0, kb1, tb); break;
+        default: small_loads<L, Walk<kWalkBoth>>(p, smem, bar, wd, i, j, kb0, kb1, tb);
       }
-      // every copy in flight has landed before anything else is put there
-      for (uint32_t l = issued >= static_cast<uint32_t>(S) ? issued - S : 0u; l < issued; ++l)
-        settle_wait(&full[l % S], (l / S) & 1u, tb);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, TN, p.a_mn, p.b_mn);
-      int s = 0, acc = 0;
-      uint32_t ph = 0, aph = 0;
-      bool ok = true;
-      for (int pb = kb0; ok && pb < kb1; pb += p.piece) {
-        const int pe = pb + p.piece < kb1 ? pb + p.piece : kb1;
-        const int blocks = (pe - pb) * p.nseg;
-        if (!mbar_wait(&tempty[acc], aph ^ 1u, wd, kSiteAccFree)) break;
-        tc_fence_after();
-        const uint32_t dtm = tmem_base + static_cast<uint32_t>(acc * TN);
-        for (int kb = 0; kb < blocks; ++kb) {
-          if (!mbar_wait(&full[s], ph, wd, kSiteStage)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * L::kStageBytes);
-          const uint32_t sb = sa + L::kABytes;
-#pragma unroll
-          for (int kk = 0; kk < L::BK / 16; ++kk)
-            umma_bf16(dtm, slice_desc(sa, p.a_mn, kk), slice_desc(sb, p.b_mn, kk), idesc, (kb | kk) != 0 ? 1u : 0u);
-          umma_commit(&empty[s]);
-          if (++s == S) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-        if (!ok) break;
-        umma_commit(&tfull[acc]);
-        if (++acc == 2) {
-          acc = 0;
-          aph ^= 1u;
-        }
+      switch (p.walk) {
+        case kWalkOne: small_products<L, Walk<kWalkOne>>(p, smem, bar, wd, tmem_base, kb0, kb1); break;
+        case kWalkRows: small_products<L, Walk<kWalkRows>>(p, smem, bar, wd, tmem_base, kb0, kb1); break;
+        case kWalkCols: small_products<L, Walk<kWalkCols>>(p, smem, bar, wd, tmem_base, kb0, kb1); break;
+        default: small_products<L, Walk<kWalkBoth>>(p, smem, bar, wd, tmem_base, kb0, kb1);
       }
       umma_commit(tdown);
       settle_wait(tdown, 0, tb);
@@ -727,7 +815,17 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
       ok = warp_waits(&tfull[acc], aph, wd, kSiteAccReady);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tacc = tmem_base + static_cast<uint32_t>(acc * TN + c0) + (static_cast<uint32_t>(q4 * 32) << 16);
+      const uint32_t tacc =
+          tmem_base + static_cast<uint32_t>(2 * acc * TN + c0) + (static_cast<uint32_t>(q4 * 32) << 16);
+      if (p.nseg > 1) {
+#pragma unroll
+        for (int c = 0; c < L::NCW; c += 16) {
+          uint32_t v[16];
+          tmem_load_row<16>(tacc + TN + c, v);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) sum[c + k] += __uint_as_float(v[k]);
+        }
+      }
 #pragma unroll
       for (int c = 0; c < L::NCW; c += 16) {
         uint32_t v[16];
@@ -753,7 +851,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
 
   __syncwarp();
   cluster_sync();  // every CTA's tile is staged
-  if (warp >= 2 && !*abort_flag) {
+  if (warp >= 2 && live && !*abort_flag) {
 #pragma unroll 1
     for (int q = q0; q < TN / GC; q += 2 * p.splits) {
       F2 v[GC / 2];
@@ -765,7 +863,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_small_kernel(cons
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (c + k < parts) {
-            const uint32_t base = map_to_rank(smem_u32(smem), static_cast<uint32_t>(c + k)) + staged_at(r, GC * q);
+            const uint32_t base = map_to_rank(smem_u32(smem), static_cast<uint32_t>(first + c + k)) + staged_at(r, GC * q);
 #pragma unroll
             for (int l = 0; l < GC / 4; ++l) a[k][l] = ld_cluster_f4(base + l * 2048u);
           }
@@ -944,7 +1042,7 @@ static cudaError_t launch_small(ProductGroup& g, int blocks, cudaStream_t stream
   }
   g.p[0].sum_from = blocks;
   return launch_dependent(kernel, g, dim3(static_cast<unsigned>(blocks + g.p[0].sum_blocks)), L::kThreads, stream,
-                          L::kSmemBytes, g.p[0].splits);
+                          L::kSmemBytes, g.cluster);
 }
 
 cudaError_t launch_product_pair(int tile, ProductParams& p, int sms, cudaStream_t stream) {

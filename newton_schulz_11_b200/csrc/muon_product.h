@@ -66,6 +66,9 @@ struct ColumnSumTask {
   int32_t cols, accumulate, slices;
 };
 
+// How a small product walks a k-block: by how many terms its operands have.
+enum ProductWalk : int { kWalkOne = 0, kWalkRows, kWalkCols, kWalkBoth };
+
 struct ProductParams {
   CUtensorMap map_a[kTerms];  // operand on the tile's M side
   CUtensorMap map_b[kTerms];  // operand on the tile's N side
@@ -73,11 +76,12 @@ struct ProductParams {
   int32_t a_mn, b_mn;         // majorness: 0 = contiguous along k, 1 = along the side
   int32_t tiles_m, tiles_n;
   int32_t nk;                 // k-blocks of the whole reduction
-  int32_t splits;             // small products: CTAs of a cluster
+  int32_t splits;             // small products: CTAs of a cluster that share a tile (a power of two)
   int32_t kb_per_split;       // large products
   int32_t piece;              // k-blocks per piece
   int32_t nseg;
-  uint8_t seg_a[8], seg_b[8]; // the terms of each segment, smallest products first
+  uint8_t seg_a[8], seg_b[8]; // large products: the terms of each segment, smallest products first
+  int32_t walk;               // small products: ProductWalk
   float* partial;             // large products: [splits][e.rows][ld_partial] for the end, or nullptr
   int64_t ld_partial, split_stride;
   unsigned long long timeout_ns;
@@ -90,7 +94,7 @@ struct ProductParams {
 // One launch of small products: the second, if any, from block first_blocks on.
 struct ProductGroup {
   ProductParams p[2];
-  int32_t first_blocks;
+  int32_t first_blocks, cluster;
 };
 
 // bf16 operand map of a matrix with rows of ld elements: boxes of 64 columns x box_rows rows.
