@@ -1086,6 +1086,234 @@ def run_adamw_reference(args, world, rank):
     print(json.dumps(line), flush=True)
 
 
+# ------------------------------------------------------------------ MLP block path
+
+MLP_WORKLOAD = "gpt2-medium-144-matrices"
+MLP_TOKENS = 8192
+MLP_ACT = "gelu_tanh"
+
+
+def mlp_layers(w, matrices=0):
+    """The MLP blocks of a workload's layers, (width, hidden) each; of its first `matrices`
+    matrices when that is not 0."""
+    shapes = w.shapes[:matrices] if matrices else w.shapes
+    return [(r, c) for r, c in shapes if r < c]
+
+
+def mlp_work(layers, tokens, ns_steps):
+    """(product FLOPs, Newton-Schulz FLOPs) of one training step: three products a matrix, the
+    forward one and the two gradients'."""
+    products = sum(3 * 2 * 2 * tokens * d * h for d, h in layers)
+    ns = sum(2 * sum(matrix_work(d, h)[k] for k in ("gram", "poly", "apply")) * ns_steps for d, h in layers)
+    return products, ns
+
+
+class MlpTraining:
+    """One training step of a stack of pre-norm MLP blocks, y = x + W2 act(W1 norm(x) + b1) + b2,
+    through the library: forward, backward from the gradient of the last y, then Muon on the
+    matrices and AdamW on the vectors.  Every buffer is made here, once."""
+
+    def __init__(self, layers, tokens, device, coeffs, lr=0.02):
+        import torch
+
+        from newton_schulz_11_b200 import api
+
+        self.api = api
+        gen = torch.Generator(device=device).manual_seed(0)
+
+        def draw(*shape, std=1.0, dtype=torch.bfloat16):
+            return (std * torch.randn(*shape, generator=gen, device=device)).to(dtype)
+
+        def empty(*shape, dtype=torch.bfloat16):
+            return torch.empty(*shape, dtype=dtype, device=device)
+
+        d0 = layers[0][0]
+        self.x, self.dy = draw(tokens, d0), draw(tokens, d0, std=1e-3)
+        self.blocks, ws, gs, vecs, vec_grads = [], [], [], [], []
+        for d, h in layers:
+            b = {"w1": draw(h, d, std=0.02), "w2": draw(d, h, std=0.02), "n": empty(tokens, d), "h": empty(tokens, h),
+                 "z": empty(tokens, h), "y": empty(tokens, d)}
+            for name, n, fill in (("gain", d, 1.0), ("beta", d, 0.0), ("b1", h, 0.0), ("b2", d, 0.0)):
+                b[name] = torch.full((n,), fill, device=device)
+                b["g_" + name] = empty(n, dtype=torch.float32)
+                vecs.append(b[name])
+                vec_grads.append(b["g_" + name])
+            for name in ("w1", "w2"):
+                b["g_" + name] = empty(*b[name].shape, dtype=torch.float32)
+                ws.append(b[name])
+                gs.append(b["g_" + name])
+            self.blocks.append(b)
+        hidden = max(h for _, h in layers)
+        self.dz, self.dn = empty(tokens * hidden), empty(tokens, d0)
+        self.dx = empty(tokens, d0)
+        self.muon = api.PreparedMuonStep(ws, gs, [torch.zeros_like(g) for g in gs], lr=lr, coeffs=coeffs)
+        self.adamw = api.PreparedAdamW(vecs, vec_grads, [torch.zeros_like(v) for v in vecs],
+                                       [torch.zeros_like(v) for v in vecs], lr=ADAMW_HYPER["lr"],
+                                       betas=(ADAMW_HYPER["beta1"], ADAMW_HYPER["beta2"]), eps=ADAMW_HYPER["eps"],
+                                       weight_decay=ADAMW_HYPER["weight_decay"])
+        self.t = 0
+
+    def layers_pass(self):
+        """Forward and backward: the gradients, and dx of the stack's input."""
+        api, x = self.api, self.x
+        for b in self.blocks:
+            b["x"] = x
+            _, b["mean"], b["rstd"] = api.layer_norm(x, b["gain"], b["beta"], out=b["n"])
+            api.linear(b["n"], b["w1"], b["b1"], act=MLP_ACT, out=b["h"], preact=b["z"])
+            x = api.linear(b["h"], b["w2"], b["b2"], residual=x, out=b["y"])
+        dy = self.dy
+        for b in reversed(self.blocks):
+            dz = self.dz[:b["z"].numel()].view(b["z"].shape)
+            api.linear_backward(dy, b["h"], b["w2"], in_act=MLP_ACT, in_preact=b["z"], dx=dz, dw=b["g_w2"],
+                                db=b["g_b2"])
+            api.linear_backward(dz, b["n"], b["w1"], dx=self.dn, dw=b["g_w1"], db=b["g_b1"])
+            # the residual's gradient joins in; from the second block on dx is both
+            api.layer_norm_backward(self.dn, b["x"], b["mean"], b["rstd"], b["gain"], skip=dy, dx=self.dx,
+                                    dgain=b["g_gain"], dbias=b["g_beta"])
+            dy = self.dx
+        return self.dx
+
+    def __call__(self, stream):
+        self.t += 1
+        self.layers_pass()
+        self.muon(stream)
+        self.adamw(self.t, stream)
+
+
+def mlp_oracle_ms(w, layers, tokens, sample_tokens=256):
+    """The fp64 oracle on one block with `sample_tokens` tokens, its layers' part scaled to all
+    tokens, and Muon on its two matrices; times the number of blocks."""
+    import numpy as np
+
+    import oracle
+    from oracle import layers_oracle as lo
+
+    d, h = layers[0]
+    rng = np.random.default_rng(0)
+    x, dy = rng.standard_normal((sample_tokens, d)), 1e-3 * rng.standard_normal((sample_tokens, d))
+    w1, w2 = 0.02 * rng.standard_normal((h, d)), 0.02 * rng.standard_normal((d, h))
+    gain, zero_d, zero_h = np.ones(d), np.zeros(d), np.zeros(h)
+    t0 = time.perf_counter()
+    n, mean, rstd = lo.layer_norm(x, gain, zero_d)
+    a, z = lo.linear(n, w1, zero_h, MLP_ACT)
+    lo.linear(a, w2, zero_d, "none", x)
+    dz, g2, _ = lo.linear_backward(dy, a, w2, MLP_ACT, z)
+    dn, g1, _ = lo.linear_backward(dz, n, w1)
+    lo.layer_norm_backward(dn, x, mean, rstd, gain, dy)
+    t1 = time.perf_counter()
+    for p, g in ((w1, g1), (w2, g2)):
+        oracle.muon_step(p, g, np.zeros_like(g), lr=w.lr, beta=w.beta, weight_decay=w.weight_decay, nesterov=w.nesterov,
+                         coeffs=load_coeffs(w))
+    t2 = time.perf_counter()
+    sample = (f"the fp64 oracle on one block: its layers on {sample_tokens} tokens, scaled to {tokens}, and Muon on "
+              f"its two matrices; times {len(layers)} blocks (AdamW on the vectors left out)")
+    return ((t1 - t0) * tokens / sample_tokens + (t2 - t1)) * 1e3 * len(layers), sample
+
+
+def mlp_config(w, layers, world):
+    d, h = layers[0]
+    return {"workload": w.name + " (MLP blocks)", "blocks": len(layers), "width": d, "hidden": h, "tokens": MLP_TOKENS,
+            "activation": MLP_ACT, "param_dtype": "bf16", "ns_steps": w.ns_steps, "schedule": w.schedule,
+            "l2": "inputs larger than L2 (activations ~%.2f GB)" % (len(layers) * MLP_TOKENS * (2 * h + 2 * d) * 2 / 1e9),
+            "parallelism": "replicas" if world > 1 else "single"}
+
+
+def run_mlp(args, world, rank, local):
+    import torch
+
+    from newton_schulz_11_b200 import api, build
+
+    build.build()
+    torch.cuda.set_device(local)
+    dev = torch.device("cuda", local)
+    w = inputs.WORKLOADS[MLP_WORKLOAD]
+    layers = mlp_layers(w, args.matrices)
+    step = MlpTraining(layers, MLP_TOKENS, dev, load_coeffs(w), lr=w.lr)
+    stream = torch.cuda.current_stream(dev)
+
+    def timed(n, one):
+        e0, e1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        barrier(world)
+        torch.cuda.synchronize()
+        e0.record(stream)
+        for _ in range(n):
+            one()
+        e1.record(stream)
+        torch.cuda.synchronize()
+        barrier(world)
+        return dist_max(e0.elapsed_time(e1) / n, world)
+
+    for _ in range(args.warmup):
+        step(stream)
+    torch.cuda.synchronize()
+    clocks = Clocks(local)
+    clocks.start()
+    clocks.mark(True)
+    ms_step = timed(args.steps, lambda: step(stream))
+    clocks.mark(False)
+    clk = clocks.stop()
+    ms_layers = timed(max(1, min(args.steps, 20)), step.layers_pass)
+    e2e = None
+    if not args.no_e2e:
+        pin_x, pin_dy = step.x.cpu().pin_memory(), step.dy.cpu().pin_memory()
+        pin_dx = torch.empty_like(pin_x).pin_memory()
+
+        def one():
+            step.x.copy_(pin_x, non_blocking=True)
+            step.dy.copy_(pin_dy, non_blocking=True)
+            step(stream)
+            pin_dx.copy_(step.dx, non_blocking=True)
+
+        e2e = {"value": round(timed(max(1, min(args.steps, 50)), one), 4), "unit": "ms",
+               "h2d_bytes_per_step": 2 * pin_x.numel() * 2, "d2h_bytes_per_step": pin_dx.numel() * 2}
+    status = api.layers_status(dev)
+    if status[0] != 0:
+        raise RuntimeError(f"layers_status {status} after the timed steps")
+    if rank != 0:
+        return
+    peaks, peak_src = load_peaks()
+    products, ns = mlp_work(layers, MLP_TOKENS, w.ns_steps)
+    line = {
+        "metric": "mlp_training_step_ms", "value": round(ms_step, 4), "unit": "ms", "n_gpus": world,
+        "steps": args.steps, "warmup": args.warmup, "ms_per_step": round(ms_step, 4), "higher_is_better": False,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": mlp_config(w, layers, world),
+        # the layers' forward and backward; their bytes are far below their FLOPs' time
+        "roofline": dict(roofline_of(products, 0, ms_layers, peaks, peak_src), kernel="forward and backward"),
+        "optimizer": {"ms": round(ms_step - ms_layers, 4), "newton_schulz_tflops":
+                      round(ns / max(ms_step - ms_layers, 1e-6) / 1e9, 1)},
+        "clocks": clk, "e2e": e2e,
+        # at least: a norm, two products and their four gradients' products, the norm's two a block
+        "gpu_launches": (9 * len(layers) + 1) * args.steps,
+    }
+    if world == 1 and not args.no_cpu_baseline:
+        cms, sample = mlp_oracle_ms(w, layers, MLP_TOKENS)
+        line["cpu_baseline"] = {"value": round(cms, 1), "unit": "ms", "cores": blas_threads(), "kind": "oracle",
+                                "sample": sample}
+    print(json.dumps(line), flush=True)
+
+
+def run_mlp_reference(args, world, rank):
+    if rank != 0:
+        return
+    w = inputs.WORKLOADS[MLP_WORKLOAD]
+    layers = mlp_layers(w, args.matrices)
+    for _ in range(args.warmup):
+        mlp_oracle_ms(w, layers, MLP_TOKENS)
+    runs = [mlp_oracle_ms(w, layers, MLP_TOKENS) for _ in range(args.steps)]
+    value = statistics.median(r[0] for r in runs)
+    line = {
+        "impl": "reference", "metric": "mlp_training_step_ms", "value": round(value, 3), "unit": "ms", "n_gpus": world,
+        "steps": args.steps, "warmup": args.warmup, "ms_per_step": round(value, 3), "higher_is_better": False,
+        "scaling": "weak", "vs_baseline": None, "dtype": "f64", "data": "synthetic",
+        "config": mlp_config(w, layers, world),
+        "cpu_baseline": {"value": round(value, 3), "unit": "ms", "cores": blas_threads(), "kind": "oracle",
+                         "sample": runs[0][1]},
+        "e2e": {"value": round(value, 3), "unit": "ms", "h2d_bytes_per_step": 0, "d2h_bytes_per_step": 0},
+    }
+    print(json.dumps(line), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -1096,8 +1324,9 @@ def main():
     ap.add_argument("--no-e2e", action="store_true",
                     help="skip the host-buffer pass (for workloads whose inputs do not fit pinned host memory)")
     ap.add_argument("--no-cpu-baseline", action="store_true")
-    ap.add_argument("--path", default="muon", choices=["muon", "adamw"],
-                    help="muon: the Muon step (default); adamw: the AdamW step of the non-matrix parameters")
+    ap.add_argument("--path", default="muon", choices=["muon", "adamw", "mlp"],
+                    help="muon: the Muon step (default); adamw: the AdamW step of the non-matrix parameters; "
+                         "mlp: a training step of the MLP blocks, forward, backward and both optimizers")
     ap.add_argument("--matrices", type=int, default=0,
                     help="run only the first K matrices of the workload (a small case of the same kernels)")
     ap.add_argument("--parallel", default="auto", choices=["auto", "single", "sharded", "replicas"],
@@ -1114,11 +1343,11 @@ def main():
     if args.impl == "reference":
         world = int(os.environ.get("WORLD_SIZE", "1"))
         rank = int(os.environ.get("RANK", "0"))
-        (run_adamw_reference if args.path == "adamw" else run_reference)(args, world, rank)
+        {"muon": run_reference, "adamw": run_adamw_reference, "mlp": run_mlp_reference}[args.path](args, world, rank)
         return
     world, rank, local = dist_setup(args)
     try:
-        (run_adamw if args.path == "adamw" else run_ours)(args, world, rank, local)
+        {"muon": run_ours, "adamw": run_adamw, "mlp": run_mlp}[args.path](args, world, rank, local)
     finally:
         if world > 1:
             import torch.distributed as dist
