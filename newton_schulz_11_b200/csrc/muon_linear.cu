@@ -27,7 +27,9 @@ struct ActGradParams {
 };
 
 // Eight columns of a row per thread and step; in whole rows of 16-column groups (p.wide) 16,
-// 32 bytes of each bf16 operand at a time.
+// 32 bytes of each bf16 operand at a time.  HBM-bound, with the instructions of the derivative
+// close behind: 16384 x 4096 bf16 GELU (tanh) in 64.7 us, 97% of the measured copy bandwidth
+// (84.8 us eight columns at a time).
 __global__ void __launch_bounds__(256, 5) muon_activation_backward_kernel(const __grid_constant__ ActGradParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -377,7 +379,9 @@ struct LinearGradPlan {
 
 // How many blocks that would be idle under the call's last product can sum the columns of dy
 // in less time than that product takes, or 0.  A block takes 256 rows of 64 columns in about
-// a microsecond (eight loads in flight a thread), a product 0.4 us a k-block.
+// a microsecond (eight loads in flight a thread), a product 0.4 us a k-block.  Measured, with
+// the sums riding and with them in the first launch (us): 515 x 770 x 1030 fp32 34.7, 41.5;
+// 1000 x 1000 x 1000 bf16 18.8, 26; 8192 x 4096 x 1024 bf16 145, 144.
 int idle_blocks(const Plan& last, const Plan& other, int64_t tasks, int64_t rows) {
   const bool pair = kTileShapes[last.tile].pair;
   const int size = pair ? 2 : static_cast<int>(last.shared ? std::max(last.splits, other.splits) : last.splits);

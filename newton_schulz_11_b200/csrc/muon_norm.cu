@@ -52,7 +52,8 @@ struct NormGradParams {
 // otherwise (odd widths, unaligned rows) its elements are TPR apart, so that a warp's
 // accesses are contiguous all the same.  The arithmetic is in fp32 pairs: on bf16 rows the
 // kernels are bound by instruction issue before memory (in scalar form the backward pass
-// took 37 instructions an element, and 209 us instead of 149 us at 32768 x 4096).
+// took 37 instructions an element, and 209 us instead of 149 us at 32768 x 4096, which rows
+// without column checks brought to 129).
 
 enum Form : int { kLoose = 0, kGroups8 = 1, kFull = 2 };  // not VEC; VEC; VEC and no thread without columns
 
@@ -179,6 +180,12 @@ __device__ __forceinline__ void join_groups(F2 (*d)[4], F2* own, int group, int 
 // 16 in its slot.  (Bytes beside the row in its first and last unit are copied, not used.)
 // A stage's refill is issued by one thread of the group after the sums of the next row,
 // which every thread reaches only when it has read this row for the last time.
+//
+// Bound by HBM where rows are long, by the issue of the row sums' instructions where a warp has
+// a short row, by the launch for few rows.  Captured calls (us, and of the measured copy
+// bandwidth): forward bf16 32768 x 4096 91.4 (91%), 32768 x 768 18.0 (87%), 8 x 768 3.1; backward
+// bf16 32768 x 4096 129 (97%), 16384 x 768 24.5 (64%, with the join of its parameter gradients),
+// fp32 1001 x 1023 with unaligned rows 9.3.
 //
 // A copy that does not land within the budget is recorded in the status word; the group
 // then carries on without waiting, so that every barrier is still met, and leaves.
@@ -692,7 +699,7 @@ struct RingSize {
 };
 
 RingSize ring_size(int64_t stage_bytes, int groups, int per_sm, int64_t least) {
-  const int64_t budget = (232448 / per_sm - 3072) / (groups * stage_bytes);
+  const int64_t budget = (232448 / per_sm - 3 * 1024) / (groups * stage_bytes);
   const int64_t stages = std::max<int64_t>(2, std::min<int64_t>(kMaxStages, budget));
   return {static_cast<int>(stages), static_cast<int>(std::max(least, stages * groups * stage_bytes))};
 }
