@@ -4,7 +4,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <vector>
 
 #include "muon_b200.h"
 #include "muon_product.h"
@@ -22,15 +21,23 @@ struct Span {
   bool written;
 };
 
-// Collects a call's operands, checking each; `status` keeps the first error.
+// Collects a call's operands, checking each; `status` keeps the first error.  (An array of the
+// most a call has: nothing here can throw through the C ABI.)
 struct Operands {
-  std::vector<Span> spans;
+  static constexpr int kMost = 10;
+  Span spans[kMost];
+  int count = 0;
   muon_status_t status = MUON_OK;
-
-  Operands() { spans.reserve(10); }
 
   void fail(muon_status_t s) {
     if (status == MUON_OK) status = s;
+  }
+
+  void put(const Span& s) {
+    if (count < kMost)
+      spans[count++] = s;
+    else
+      fail(MUON_ERR_INVALID_ARG);
   }
 
   // `required` views must have data; an absent optional one is skipped.
@@ -47,7 +54,7 @@ struct Operands {
     if (rows == 0) return;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(v.data);
     const uintptr_t bytes = static_cast<uintptr_t>(((rows - 1) * ld + cols) * static_cast<int64_t>(e));
-    spans.push_back({lo, lo + bytes, static_cast<uintptr_t>(ld) * e, static_cast<uintptr_t>(cols) * e, rows, written});
+    put({lo, lo + bytes, static_cast<uintptr_t>(ld) * e, static_cast<uintptr_t>(cols) * e, rows, written});
   }
 
   void add_f32(const float* p, int64_t n, bool required, bool written) {
@@ -59,7 +66,7 @@ struct Operands {
   void add_bytes(const void* p, size_t n) {
     if (n > 0) {
       const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-      spans.push_back({lo, lo + n, n, n, 1, true});
+      put({lo, lo + n, n, n, 1, true});
     }
   }
 
@@ -80,8 +87,8 @@ struct Operands {
   // No written operand may share bytes with another.
   muon_status_t check() const {
     if (status != MUON_OK) return status;
-    for (size_t i = 0; i < spans.size(); ++i)
-      for (size_t j = i + 1; j < spans.size(); ++j)
+    for (int i = 0; i < count; ++i)
+      for (int j = i + 1; j < count; ++j)
         if ((spans[i].written || spans[j].written) && meet(spans[i], spans[j])) return MUON_ERR_INVALID_ARG;
     return MUON_OK;
   }
