@@ -11,6 +11,10 @@ Tolerances, element by element, from the arithmetic (u = 2^-24, half a step of f
   activations       2^-20 + z^2 2^-21 relative (exp, reciprocal and erfc to a few units, and
                     the rounding of their arguments, which weighs up to z^2)
   slopes            2^-19 (1 + |slope|)"""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -760,3 +764,63 @@ def test_refusals_name_the_argument():
         api.layer_norm(x, eps=float("nan"))
     with pytest.raises(api.MuonError):  # in place over the input is not offered
         api.layer_norm(x, out=x)
+
+
+# sizes whose two products are small and share a launch: evenly, with different splits, with
+# CTAs of the last cluster left over, and ragged
+@pytest.mark.parametrize("xt,wt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,n_in,n_out", [(256, 640, 896), (130, 384, 640), (300, 520, 384), (512, 256, 1152),
+                                             (1000, 136, 648), (129, 1160, 264), (777, 333, 259)])
+def test_two_products_in_one_launch(rows, n_in, n_out, xt, wt):
+    require_gpu()
+    from newton_schulz_11_b200 import api
+
+    gen = torch.Generator(device="cuda").manual_seed(rows * n_out + n_in)
+
+    def mk(r, c, dt, std):
+        return (torch.randn(r, c, generator=gen, device="cuda") * std).to(DT[dt])
+
+    dy, x, w = mk(rows, n_out, xt, 0.1), mk(rows, n_in, xt, 1.0), mk(n_out, n_in, wt, n_in ** -0.5)
+    dx, dw, db = api.linear_backward(dy, x, w)
+    g = dy.double()
+    rdx, rdw, rdb = g @ w.double(), g.t() @ x.double(), g.sum(0)
+    half = HALF[DT[xt]]
+    close64(dx, rdx, tol64(g, w.double().t(), n_out) + (half + 2 * U) * rdx.abs() + 1e-38, "dx")
+    close64(dw, rdw, tol64(g.t(), x.double().t(), rows) + 2 * U * rdw.abs(), "dw")
+    close64(db, rdb, (rows / 2 + 40) * U * g.abs().sum(0) + 2 * U * rdb.abs(), "db")
+
+
+def test_first_calls_of_a_process_are_captured():
+    """Nothing has to run before the capture: the kernels load, the plans are made and the
+    scratch is taken inside it."""
+    require_gpu()
+    code = """
+import torch
+from newton_schulz_11_b200 import api
+torch.manual_seed(0)
+x = torch.randn(200, 264, device="cuda")
+w1, w2 = torch.randn(520, 264, device="cuda") / 16, torch.randn(264, 520, device="cuda").bfloat16() / 16
+gain = torch.ones(264, device="cuda")
+def step():
+    n, mean, rstd = api.layer_norm(x, gain)
+    h, z = api.linear(n, w1, act="gelu", save_preact=True)
+    y = api.linear(h, w2, residual=x)
+    dz, dw2, db2 = api.linear_backward(y, h, w2, in_act="gelu", in_preact=z)
+    dn, dw1, db1 = api.linear_backward(dz, n, w1)
+    a = api.activation_backward(dz, z, "silu")
+    return [y, dw2, db2, dw1, db1, a, *api.layer_norm_backward(dn, x, mean, rstd, gain, skip=y)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = step()
+for t in out:
+    t.fill_(float("nan"))
+g.replay()
+x.copy_(x.flip(0))
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, step()))
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
