@@ -426,7 +426,9 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
   if (d->db != nullptr) {
     const int64_t tasks = ceil_div(d->out, 64);
     pl.sum_blocks = dx || dw ? idle_blocks(dw ? pl.dw : pl.dx, pl.dx, tasks, d->rows) : 0;
-    pl.slices = pl.sum_blocks > 0 ? 1 : std::max<int64_t>(1, std::min(d->rows / 512, 8 * kSms / tasks));
+    // a block's 256 threads cover 256 rows of 64 columns in one batch of loads (512 rows a
+    // block: 7.9 us for 2000 x 2000 fp32 instead of 5.4, 7.6 for 8192 x 1024 bf16 instead of 6.4)
+    pl.slices = pl.sum_blocks > 0 ? 1 : std::max<int64_t>(1, std::min(d->rows / 256, 8 * kSms / tasks));
     pl.db_at = pl.bytes;
     if (pl.slices > 1) pl.bytes += up(static_cast<size_t>(pl.slices) * d->out * 4);
   }
