@@ -379,9 +379,9 @@ struct LinearGradPlan {
 
 // How many blocks that would be idle under the call's last product can sum the columns of dy
 // in less time than that product takes, or 0.  A block takes 256 rows of 64 columns in about
-// a microsecond (eight loads in flight a thread), a product 0.4 us a k-block.  Measured, with
-// the sums riding and with them in the first launch (us): 515 x 770 x 1030 fp32 34.7, 41.5;
-// 1000 x 1000 x 1000 bf16 18.8, 26; 8192 x 4096 x 1024 bf16 145, 144.
+// a microsecond, a product 0.4 us a k-block.  Measured, with the sums riding and with them in
+// the first launch (us): 515 x 770 x 1030 fp32 33.8, 39.0; 1000 x 1000 x 1000 bf16 18, 21.8;
+// 8192 x 4096 x 1024 bf16 132 to 135, 140.
 int idle_blocks(const Plan& last, const Plan& other, int64_t tasks, int64_t rows) {
   const bool pair = kTileShapes[last.tile].pair;
   const int size = pair ? 2 : static_cast<int>(last.shared ? std::max(last.splits, other.splits) : last.splits);
@@ -427,7 +427,7 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
     const int64_t tasks = ceil_div(d->out, 64);
     pl.sum_blocks = dx || dw ? idle_blocks(dw ? pl.dw : pl.dx, pl.dx, tasks, d->rows) : 0;
     // a block's 256 threads cover 256 rows of 64 columns in one batch of loads (512 rows a
-    // block: 7.9 us for 2000 x 2000 fp32 instead of 5.4, 7.6 for 8192 x 1024 bf16 instead of 6.4)
+    // block: 7.9 us for 2000 x 2000 fp32 where 256 took 5.4; 7.6 and 6.4 for 8192 x 1024 bf16)
     pl.slices = pl.sum_blocks > 0 ? 1 : std::max<int64_t>(1, std::min(d->rows / 256, 8 * kSms / tasks));
     pl.db_at = pl.bytes;
     if (pl.slices > 1) pl.bytes += up(static_cast<size_t>(pl.slices) * d->out * 4);
