@@ -258,7 +258,8 @@ void add_pack(PrepareParams* p, const Operand& o, uint8_t* ws) {
   t.term_stride = static_cast<int64_t>(o.term_bytes() / 2);
   t.cols = static_cast<int32_t>(o.cols);
   t.terms = o.terms;
-  t.sweep = make_sweep(o.rows, o.ld_packed / 8, 8 * kSms);
+  t.sweep = make_sweep(ceil_div(o.rows, 2), o.ld_packed / 8, 8 * kSms);  // two rows a thread
+  t.sweep.rows = o.rows;
   p->begin[p->packs + 1] = p->begin[p->packs] + sweep_blocks(t.sweep);
   ++p->packs;
 }

@@ -8,7 +8,7 @@
 // launch.
 //
 // Operand precision.  A bf16 operand is read as it is.  An fp32 operand comes as three bf16
-// terms, x = h + m + l exactly (pack_group), and the product as the sum of the term products
+// terms, x = h + m + l exactly (pack_terms), and the product as the sum of the term products
 // whose size is at least 2^-16 of the whole: h h, h m, m h, m m, h l, l h (six), or h b, m b,
 // l b against a bf16 operand (three).  The large products walk the k-blocks of a piece once
 // per term product, the smallest first, all into one accumulator (a second one would not fit
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) muon_product_pair_kernel(const
 //
 // Measured (captured calls, us): 1 x 1024 x 4096 6.5, 1 x 4096 x 4096 13 (2.6 TB/s of weights),
 // 16 x 4096 x 14336 30 (3.9 TB/s), 512 x 1024 x 4096 12.4; both gradients of 256 x 768 x 768 with
-// fp32 weights 12.9, with the layout of the terms.
+// fp32 weights 12.3, with the layout of the terms.
 template <int TN_, bool FLIP_>
 struct Small {
   static constexpr int TN = TN_;
@@ -955,26 +955,69 @@ __device__ __forceinline__ void run_sweep(const Sweep& s, int b, F&& f) {
 // hold the 24 bits of an fp32 value exactly and none overflows (only terms below 2^-133 are
 // lost).  What is not finite goes into h alone.  A bf16 source is copied to rows that TMA can read.
 // Bound by HBM for large operands and by the launch for small ones: 4 bytes read and 6 written
-// an element, under 3 us of the 12.9 of both gradients of 256 x 768 x 768.
-__device__ __forceinline__ void pack_group(const PackTask& p, int64_t r, int g) {
-  const int c = g * 8;
-  float x[8];
-  load_segment<8>(p.src, r * p.src.ld + c, p.cols - c, x);
+// an element, about 2 us of the 12.3 of both gradients of 256 x 768 x 768.  Testing for what is
+// not finite once for eight elements, and two rows at a time, took x W^T of 4096 x 1024 x 1024 in
+// fp32 from 56 to 47 us and both gradients of 1000 x 1000 x 1000 from 42.5 to 37.
+__device__ __forceinline__ void pack_terms(const PackTask& p, int64_t at, float (&x)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  const bool finite = top < 0x7F800000u;  // all eight: then a term is a few instructions a pair
   for (int t = 0; t < p.terms; ++t) {
     uint32_t w[4];
+    if (finite) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = __float_as_uint(x[j]);
-      uint32_t hi = b >> 16;
-      if ((b & 0x7F800000u) == 0x7F800000u) {
-        if (b & 0x007FFFFFu) hi |= 0x40u;  // a NaN stays one
-        x[j] = 0.f;
-      } else {
-        x[j] -= __uint_as_float(b & 0xFFFF0000u);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = __float_as_uint(x[2 * j]), b = __float_as_uint(x[2 * j + 1]);
+        w[j] = __byte_perm(a, b, 0x7632);
+        x[2 * j] -= __uint_as_float(a & 0xFFFF0000u);
+        x[2 * j + 1] -= __uint_as_float(b & 0xFFFF0000u);
       }
-      w[j >> 1] = (j & 1) ? (w[j >> 1] | (hi << 16)) : hi;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(x[j]);
+        uint32_t hi = b >> 16;
+        if ((b & 0x7F800000u) == 0x7F800000u) {
+          if (b & 0x007FFFFFu) hi |= 0x40u;  // a NaN stays one
+          x[j] = 0.f;
+        } else {
+          x[j] -= __uint_as_float(b & 0xFFFF0000u);
+        }
+        w[j >> 1] = (j & 1) ? (w[j >> 1] | (hi << 16)) : hi;
+      }
     }
-    *reinterpret_cast<uint4*>(p.dst + t * p.term_stride + r * p.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p.dst + t * p.term_stride + at) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Two rows a thread and step, so that two loads are on their way.
+__device__ __forceinline__ void pack_rows(const PackTask& p, int b) {
+  const Sweep& s = p.sweep;
+  const int along = 1 << s.shift, deep = 256 >> s.shift;
+  const int rb = b / s.col_blocks, cb = b - rb * s.col_blocks;
+  const int g0 = (cb << s.shift) + (threadIdx.x & (along - 1));
+  const int64_t step = static_cast<int64_t>(s.row_blocks) * deep;
+  const bool wide = !p.src.bf16 && p.src.vec > 0;
+  for (int64_t r = static_cast<int64_t>(rb) * deep + (threadIdx.x >> s.shift); r < s.rows; r += 2 * step) {
+    const bool two = r + step < s.rows;
+    for (int g = g0; g < s.groups; g += s.col_blocks << s.shift) {
+      const int c = g * 8;
+      float x[8], y[8];
+      if (wide && c + 8 <= p.cols) {
+        const float* at = static_cast<const float*>(p.src.p) + r * p.src.ld + c;
+        const float* next = two ? at + step * p.src.ld : at;
+        const float4 x0 = *reinterpret_cast<const float4*>(at), x1 = *reinterpret_cast<const float4*>(at + 4);
+        const float4 y0 = *reinterpret_cast<const float4*>(next), y1 = *reinterpret_cast<const float4*>(next + 4);
+        x[0] = x0.x, x[1] = x0.y, x[2] = x0.z, x[3] = x0.w, x[4] = x1.x, x[5] = x1.y, x[6] = x1.z, x[7] = x1.w;
+        y[0] = y0.x, y[1] = y0.y, y[2] = y0.z, y[3] = y0.w, y[4] = y1.x, y[5] = y1.y, y[6] = y1.z, y[7] = y1.w;
+      } else {
+        load_segment<8>(p.src, r * p.src.ld + c, p.cols - c, x);
+        if (two) load_segment<8>(p.src, (r + step) * p.src.ld + c, p.cols - c, y);
+      }
+      pack_terms(p, r * p.ld_dst + c, x);
+      if (two) pack_terms(p, (r + step) * p.ld_dst + c, y);
+    }
   }
 }
 
@@ -986,8 +1029,7 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
   while (static_cast<int>(blockIdx.x) >= p.begin[i + 1]) ++i;
   const int b = static_cast<int>(blockIdx.x) - p.begin[i];
   if (i < p.packs) {
-    const PackTask& t = p.pack[i];
-    run_sweep(t.sweep, b, [&](int64_t r, int g) { pack_group(t, r, g); });
+    pack_rows(p.pack[i], b);
   } else {
     column_sums<8>(p.sum, b, red);
   }
