@@ -87,8 +87,15 @@ bool act_ok(int act) { return act >= MUON_ACT_NONE && act <= MUON_ACT_SILU; }
 // k-blocks per piece of a Sum variant: 512 of k for bf16 operands, 256 where a k-block is
 // several term products, which hide the reading of the accumulator as well.  (fp32 products
 // 512 at a time are off by 5e-7 relative and 1% quicker; 256 by 2.8e-7; 128 by 1.8e-7, 3 to 5%
-// slower.)
-int64_t piece_blocks(int nseg) { return nseg == 1 ? 8 : 4; }
+// slower.)  A bf16 result does not show that much: its large products take 2048 at a time,
+// off by 2.3e-6, which cost 1% of 4096 x 16384 x 4096 (431 and 435 us).
+int64_t piece_blocks(int nseg, bool pair, bool bf16_out) { return pair && bf16_out ? 32 : nseg == 1 ? 8 : 4; }
+
+// The longest reduction of a bf16 result that stays in the accumulator as a whole: there the
+// truncation has grown to 4.5e-6 relative for zero-mean products, 1.3e-5 for products of one
+// sign (a 300th of the result's half step, 2^-8), and pieces of 2048 would cost
+// 8192 x 4096 x 14336 2% and 8192 x 4096 x 1024 with a residual 8%.
+constexpr int64_t kWholeReduction = 4096;
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -132,7 +139,7 @@ int segments(int ta, int tb) { return ta == 1 ? tb : (tb == 1 ? ta : kMaxSegment
 // What a plan depends on besides the sizes.
 struct PlanTraits {
   int nseg;      // term products
-  bool sum;      // some output is fp32
+  bool sum;      // the reduction is added in pieces
   bool tokens;   // the output's rows are tokens
   bool aligned;  // the epilogue's rows can be accessed 16 bytes at a time
 };
@@ -307,7 +314,8 @@ muon_status_t make_product(const Plan& pl, const Operand& a, bool a_mn, const Op
   p.nk = static_cast<int32_t>(pl.nk);
   p.splits = static_cast<int32_t>(pl.splits);
   p.kb_per_split = static_cast<int32_t>(pl.kb_per_split);
-  p.piece = shape.sum ? static_cast<int32_t>(piece_blocks(pl.nseg)) : p.kb_per_split;
+  const bool bf16_out = e.out.bf16 && (e.preact.p == nullptr || e.preact.bf16);
+  p.piece = shape.sum ? static_cast<int32_t>(piece_blocks(pl.nseg, shape.pair, bf16_out)) : p.kb_per_split;
   p.nseg = pl.nseg;
   p.walk = am.terms == 1 ? (bm.terms == 1 ? kWalkOne : kWalkCols) : (bm.terms == 1 ? kWalkRows : kWalkBoth);
   for (int g = 0; g < pl.nseg; ++g) {  // the smallest products first
@@ -351,7 +359,9 @@ bool wide_rows(const muon_view_t& v, int64_t rows, int64_t cols) {
   return v.data == nullptr || epi_view(v, rows, cols).vec > 0;
 }
 
-bool wants_sum(const muon_view_t& out) { return out.data != nullptr && out.dtype == MUON_F32; }
+bool wants_sum(const muon_view_t& out, int64_t k) {
+  return out.data != nullptr && (out.dtype == MUON_F32 || k > kWholeReduction);
+}
 
 struct LinearPlan {
   Operand x, w;
@@ -367,7 +377,8 @@ LinearPlan plan_linear(const muon_linear_t* d) {
   const bool aligned = wide_rows(d->y, d->rows, d->out) && wide_rows(d->preact, d->rows, d->out) &&
                        wide_rows(d->residual, d->rows, d->out);
   pl.z = make_plan(d->rows, d->out, d->in, {segments(pl.x.terms, pl.w.terms),
-                                            wants_sum(d->y) || wants_sum(d->preact), true, aligned});
+                                            wants_sum(d->y, d->in) || wants_sum(d->preact, d->in), true,
+                                            aligned});
   pl.x.place(&pl.bytes);
   pl.w.place(&pl.bytes);
   pl.partial_at = pl.bytes;
@@ -415,7 +426,8 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
     pl.w.place(&pl.bytes);
     dx_aligned = wide_rows(d->dx, d->rows, d->in) && wide_rows(d->skip, d->rows, d->in) &&
                  (d->in_act == MUON_ACT_NONE || wide_rows(d->preact, d->rows, d->in));
-    pl.dx = make_plan(d->rows, d->in, d->out, {segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx), true, dx_aligned});
+    pl.dx = make_plan(d->rows, d->in, d->out,
+                      {segments(pl.dy.terms, pl.w.terms), wants_sum(d->dx, d->out), true, dx_aligned});
   }
   if (dw) {
     pl.x = Operand(d->x, d->rows, d->in);

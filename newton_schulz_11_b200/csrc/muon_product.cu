@@ -16,10 +16,12 @@
 //
 // Sums.  The tensor cores add 16 products at a time to the fp32 accumulator and truncate.
 // Left alone that costs about 1.1e-9 K relative for zero-mean data (measured: 9e-6 at
-// K = 8192, 1.9e-5 at K = 16384), far below a bf16 output's half step but not below fp32's.
-// The Sum variants and the small products therefore end the accumulation after 512 of k (5e-7
-// by the same rate; 256 where an operand is fp32, measured 2.8e-7), read the accumulator into
-// registers and add it there with rounding to nearest.
+// K = 8192, 1.9e-5 at K = 16384) and up to 6e-9 K for products of one sign (1.3e-5 at K = 4096,
+// 7.8e-4 at K = 131072): far below a bf16 output's half step up to K = 4096 but not below
+// fp32's.  The Sum variants and the small products therefore end the accumulation after 512 of
+// k (5e-7 by the same rate; 256 where an operand is fp32, measured 2.8e-7), read the accumulator
+// into registers and add it there with rounding to nearest; large products with bf16 results
+// do so after 2048 of k where the reduction is longer than 4096.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -1,0 +1,48 @@
+"""Calls of the layers that once gave a wrong answer, on the GPU: each test fails on the code
+that had the fault.
+
+Tolerances as in test_gpu_layers.py, counted in u = 2^-24, half a step of fp32."""
+import numpy as np
+import pytest
+
+from oracle import layers_oracle as lo
+from tests.gpu_util import require_gpu, torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+@pytest.mark.parametrize("cols", [2048, 2050])
+def test_long_reductions_into_bf16_do_not_drift(cols):
+    """The tensor cores truncate when they add 16 products to the accumulator; for products of one
+    sign that is a drift, of less than two steps 2^-23 of the running sum each time.  In pieces
+    of 2048 of k (128 additions), with a running sum that is half of the piece's on average, the
+    result is too small by at most 128 * 2^-23 = 1.5e-5 relative; 2^17 of k in one piece lost
+    7.8e-4.  The results' own rounding to bf16 is as often up as down (rows and columns are
+    scaled so that the results spread over more than an octave): its mean over N results has a
+    deviation of at most 2^-8 / sqrt(3 N), counted five times.  2048 columns take the plain
+    tiles, 2050 the flipped ones."""
+    require_gpu()
+    from newton_schulz_11_b200 import api
+
+    rows, k = 2304, 1 << 17
+    gen = torch.Generator(device="cuda").manual_seed(17)
+
+    def mk(n):
+        t = torch.rand(n, k, generator=gen, device="cuda").add_(0.5)
+        return t.mul_(torch.exp2(torch.rand(n, 1, generator=gen, device="cuda"))).bfloat16()
+
+    x, w = mk(rows), mk(cols)
+    got = {"y": api.linear(x, w), "dx": api.linear_backward(x, w.new_empty(rows, cols), w.t().contiguous(),
+                                                            need_dw=False, need_db=False)[0]}
+    want = torch.zeros(rows, cols, device="cuda", dtype=torch.float64)
+    for i in range(0, k, 8192):
+        want += x[:, i:i + 8192].double() @ w[:, i:i + 8192].double().t()
+    for name, y in got.items():
+        drift = float(((y.double() - want) / want).mean())
+        assert abs(drift) <= 128 * 2.0 ** -23 + 5 * 2.0 ** -8 / (3 * want.numel()) ** 0.5, (name, drift)
