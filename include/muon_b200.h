@@ -316,9 +316,11 @@ muon_status_t muon_newton_schulz_static(const muon_matrix_t* mats, int n, int ns
  * Results do not depend on the order in which blocks run: no atomics on data.
  *
  * Execution, ownership and errors are those of the header's opening comment, with two
- * differences: the workspace holds nothing between calls and needs no muon_workspace_init,
- * and device-side waits that run out are recorded in one status word per device, read with
- * muon_layers_status.  Calls that may overlap on the GPU need workspaces of their own.
+ * differences: the workspace holds nothing between calls and needs no muon_workspace_init
+ * (its first 256 bytes are left alone, so that a region initialised for muon_step keeps that
+ * call's status word and may serve both), and device-side waits that run out are recorded in
+ * one status word per device, read with muon_layers_status.  Calls that may overlap on the
+ * GPU need workspaces of their own.
  */
 typedef enum {
   MUON_ACT_NONE = 0,

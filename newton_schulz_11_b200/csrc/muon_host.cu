@@ -39,7 +39,6 @@ static_assert(sizeof(muon_matrix_t) == 80, "muon_matrix_t layout");
 static_assert(sizeof(FinalParams) < 32000, "kernel parameter block too large");
 static_assert(sizeof(EwParams) < 32000, "kernel parameter block too large");
 
-constexpr size_t kHeaderBytes = 256;
 constexpr size_t kBufAlign = 1024;
 constexpr int64_t kChunkElems = 16384;
 constexpr int kStagedApplyMaxM = 1024;  // Gram side up to which the staged (64-deep) variants serve

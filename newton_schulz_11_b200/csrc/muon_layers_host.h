@@ -123,6 +123,10 @@ cudaError_t norm_status(int32_t (&out)[2], bool clear, cudaStream_t s);
 
 inline muon_status_t queued(cudaError_t e) { return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA; }
 
+// The start of a workspace: the step's status word and counts (muon_workspace_init).  The
+// layers leave it alone, so that one region can serve both.
+constexpr size_t kHeaderBytes = 256;
+
 constexpr int64_t kMaxSide = int64_t(1) << 24;  // columns, features (as for muon_matrix_t)
 constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens
 

@@ -7,7 +7,8 @@
 //
 // Workspace: the operands that the tensor cores cannot read in place (fp32 ones, as bf16
 // terms; bf16 ones whose rows are not 16-byte aligned, copied), the partial sums of split
-// reductions, and those of the bias gradient.  Nothing in it outlives the call.
+// reductions, and those of the bias gradient, behind the step's header (kHeaderBytes).  Nothing
+// in it outlives the call.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -366,12 +367,13 @@ bool wants_sum(const muon_view_t& out, int64_t k) {
 struct LinearPlan {
   Operand x, w;
   Plan z;
-  size_t partial_at = 0, bytes = 0;
+  size_t partial_at = 0, bytes = 0;  // from the start of the workspace, whose header is left alone
 };
 
 LinearPlan plan_linear(const muon_linear_t* d) {
   LinearPlan pl;
   if (d->rows == 0) return pl;
+  pl.bytes = kHeaderBytes;
   pl.x = Operand(d->x, d->rows, d->in);
   pl.w = Operand(d->w, d->out, d->in);
   const bool aligned = wide_rows(d->y, d->rows, d->out) && wide_rows(d->preact, d->rows, d->out) &&
@@ -383,6 +385,7 @@ LinearPlan plan_linear(const muon_linear_t* d) {
   pl.w.place(&pl.bytes);
   pl.partial_at = pl.bytes;
   pl.bytes += pl.z.partial_bytes;
+  if (pl.bytes == kHeaderBytes) pl.bytes = 0;
   return pl;
 }
 
@@ -419,6 +422,7 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
   if (d->rows == 0) return pl;
   const bool dx = d->dx.data != nullptr, dw = d->dw.data != nullptr;
   bool dx_aligned = true;
+  pl.bytes = kHeaderBytes;
   pl.dy = Operand(d->dy, d->rows, d->out);
   if (dx || dw) pl.dy.place(&pl.bytes);
   if (dx) {
@@ -450,6 +454,7 @@ LinearGradPlan plan_linear_grad(const muon_linear_grad_t* d) {
     pl.db_at = pl.bytes;
     if (pl.slices > 1) pl.bytes += up(static_cast<size_t>(pl.slices) * d->out * 4);
   }
+  if (pl.bytes == kHeaderBytes) pl.bytes = 0;
   return pl;
 }
 

@@ -755,7 +755,7 @@ int slices_for(const muon_layer_norm_grad_t* d) {
 
 size_t norm_grad_bytes(const muon_layer_norm_grad_t* d) {
   if ((d->dgain == nullptr && d->dbias == nullptr) || d->rows == 0) return 0;
-  return static_cast<size_t>(slices_for(d)) * 2 * static_cast<size_t>(d->cols) * sizeof(float);
+  return kHeaderBytes + static_cast<size_t>(slices_for(d)) * 2 * static_cast<size_t>(d->cols) * sizeof(float);
 }
 
 }  // namespace
@@ -860,7 +860,7 @@ extern "C" muon_status_t muon_layer_norm_backward(const muon_layer_norm_grad_t* 
   p.rstd = d->rstd;
   p.dgain = d->dgain;
   p.dbias = d->dbias;
-  p.partial = grads ? static_cast<float*>(workspace) : nullptr;
+  p.partial = grads ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes) : nullptr;
   p.rows = d->rows;
   p.cols = static_cast<int32_t>(d->cols);
   p.accumulate = d->accumulate;

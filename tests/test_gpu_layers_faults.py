@@ -46,3 +46,36 @@ def test_long_reductions_into_bf16_do_not_drift(cols):
     for name, y in got.items():
         drift = float(((y.double() - want) / want).mean())
         assert abs(drift) <= 128 * 2.0 ** -23 + 5 * 2.0 ** -8 / (3 * want.numel()) ** 0.5, (name, drift)
+
+
+def test_a_workspace_shared_with_the_step_keeps_its_status():
+    """The step records a non-finite gradient in the workspace's first bytes, once, until they
+    are cleared: layers that use the same workspace neither overwrite nor block that."""
+    require_gpu()
+    from newton_schulz_11_b200 import _lib, api
+
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def mk(r, c):
+        return torch.randn(r, c, generator=gen, device="cuda")
+
+    ws = api.Workspace(torch.device("cuda", torch.cuda.current_device()))
+    ws.ensure(64 << 20, torch.cuda.current_stream().cuda_stream)
+    p, g, m = mk(96, 64).bfloat16(), mk(96, 64), torch.zeros(96, 64, device="cuda")
+    x, w, dy = mk(700, 520), mk(264, 520), mk(700, 264)
+    _, mean, rstd = api.layer_norm(x)
+
+    def layers(workspace):
+        return [api.linear(x, w, workspace=workspace), *api.linear_backward(dy, x, w, workspace=workspace),
+                *api.layer_norm_backward(x, x, mean, rstd, workspace=workspace)]
+
+    want = layers(None)
+    for a, b in zip(layers(ws), want):
+        assert torch.equal(a, b)
+    assert api.device_status(ws) == (_lib.MUON_OK, 0) and api.nonfinite_count(ws) == 0
+    g[5, 7] = float("nan")
+    api.muon_step([p], [g], [m], lr=0.02, workspace=ws)
+    assert api.device_status(ws) == (_lib.MUON_ERR_NONFINITE, 0) and api.nonfinite_count(ws) == 1
+    for a, b in zip(layers(ws), want):
+        assert torch.equal(a, b)
+    assert api.device_status(ws) == (_lib.MUON_ERR_NONFINITE, 0) and api.nonfinite_count(ws) == 1
