@@ -10,6 +10,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Device.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -136,6 +137,27 @@ void check(muon_status_t st, const char* where) {
   throw python_error();
 }
 
+// A new reference that is dropped at the end of the scope.
+struct Held {
+  PyObject* o;
+  explicit Held(PyObject* p) : o(p) {}
+  ~Held() { Py_XDECREF(o); }
+  Held(const Held&) = delete;
+};
+
+// A Workspace on another device would hand its memory to kernels on this one.
+void check_workspace(PyObject* w, c10::Device device) {
+  const Held on(PyObject_GetAttrString(w, "device")), buf(PyObject_GetAttrString(w, "buf"));
+  if (on.o == nullptr || buf.o == nullptr || !THPDevice_Check(on.o)) {
+    PyErr_Clear();
+    refuse(PyExc_TypeError, "workspace must be a Workspace");
+  }
+  c10::Device at = reinterpret_cast<THPDevice*>(on.o)->device;  // without an index: where its buffer is, if it has one
+  if (THPVariable_Check(buf.o)) at = THPVariable_Unpack(buf.o).device();
+  if (at.type() != device.type() || (at.has_index() && at.index() != device.index()))
+    refuse(PyExc_ValueError, "workspace is on " + at.str() + ", expected " + device.str());
+}
+
 // The call's scratch: from the caller's Workspace, or from the allocator on this stream.
 struct Scratch {
   void* ptr = nullptr;
@@ -143,6 +165,7 @@ struct Scratch {
   at::Tensor buf;
 
   Scratch(size_t need, PyObject* workspace, c10::Device device, void* stream) : bytes(need) {
+    if (given(workspace)) check_workspace(workspace, device);
     if (need == 0) return;
     if (given(workspace)) {
       PyObject* r = PyObject_CallMethod(workspace, "ensure", "nK", static_cast<Py_ssize_t>(need),

@@ -11,7 +11,8 @@ with `reshape`); bf16 and fp32 may be mixed as each function says.  Work is queu
 `stream`, by default the current stream of the tensors' device; outputs and scratch that a
 call allocates come from PyTorch's allocator on that stream, so calls on different streams
 and captured graphs share nothing.  A `workspace` given is the caller's to keep to one call
-at a time; it may be the one that `muon_step` uses, whose status the layers leave alone.
+at a time, on the tensors' device; it may be the one that `muon_step` uses, whose status the
+layers leave alone.
 """
 from __future__ import annotations
 

@@ -79,3 +79,35 @@ def test_a_workspace_shared_with_the_step_keeps_its_status():
     for a, b in zip(layers(ws), want):
         assert torch.equal(a, b)
     assert api.device_status(ws) == (_lib.MUON_ERR_NONFINITE, 0) and api.nonfinite_count(ws) == 1
+
+
+def test_a_workspace_elsewhere_is_refused():
+    """Before anything is queued, also by calls that need no scratch."""
+    require_gpu()
+    from newton_schulz_11_b200 import api
+
+    x, w, dy = (torch.ones(s, device="cuda") for s in ((40, 64), (96, 64), (40, 96)))
+    mean, rstd = torch.zeros(40, device="cuda"), torch.ones(40, device="cuda")
+    here = torch.cuda.current_device()
+
+    def calls(ws):
+        yield lambda: api.linear(x, w, workspace=ws)
+        yield lambda: api.linear(x.bfloat16(), w.bfloat16(), workspace=ws)
+        yield lambda: api.linear_backward(dy, x, w, workspace=ws)
+        yield lambda: api.layer_norm_backward(x, x, mean, rstd, workspace=ws)
+
+    moved = api.Workspace("cuda")
+    moved.buf = torch.empty(1 << 20, dtype=torch.uint8)  # its buffer says where it is
+    for ws in (api.Workspace(f"cuda:{here + 1}"), api.Workspace("cpu"), moved):
+        for call in calls(ws):
+            with pytest.raises(ValueError, match="workspace is on"):
+                call()
+        assert ws is moved or ws.buf is None
+    for call in calls("scratch"):
+        with pytest.raises(TypeError, match="must be a Workspace"):
+            call()
+    for ws in (api.Workspace("cuda"), api.Workspace(f"cuda:{here}")):
+        for _ in range(2):  # without and with a buffer
+            for call in calls(ws):
+                call()
+        assert ws.buf.device == x.device
