@@ -4,8 +4,8 @@
 //   h = (x - mean) rstd,  q = dy gain
 //   dx = rstd (q - avg(q) - h avg(q h)) + skip,  dgain = sum_rows dy h,  dbias = sum_rows dy
 //
-// The variance is summed from the centred values, never as E[x^2] - mean^2, which cancels
-// where the mean is large.
+// The variance is summed from the centred values, never as E[x^2] - mean^2, and h is formed
+// from the difference, never as x rstd - mean rstd: both cancel where the mean is large.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -447,8 +447,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kBackward) muon_layer_norm_bac
       nmean = p.mean[r + step];
       nrstd = p.rstd[r + step];
     }
-    // h = x rstd - mean rstd in one operation; past the last column dy is 0 and h harmless
-    const F2 scale = pair(rstd), shift = pair(-mean * rstd);
+    // h = (x - mean) rstd, the difference first: x rstd - mean rstd in one operation would lose
+    // |mean| rstd 2^-24 of h.  Past the last column dy is 0 and h harmless.
+    const F2 scale = pair(rstd), shift = pair(-mean);
     ring.wait(s, phase);
     const uint8_t* xrow = ring.stage(s) + within_unit<L>(row_address(p.x, r));
     const uint8_t* dyrow = ring.stage(s) + slot + within_unit<L>(row_address(p.dy, r));
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kBackward) muon_layer_norm_bac
       staged_group<L>(dyrow, L::BF16, k, t, p.cols, dy);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const F2 h = fma2(x[j], scale, shift), q = mul2(dy[j], gain[k][j]);
+        const F2 h = mul2(add2(x[j], shift), scale), q = mul2(dy[j], gain[k][j]);
         dgain[k][j] = fma2(dy[j], h, dgain[k][j]);
         dbias[k][j] = add2(dbias[k][j], dy[j]);
         aq2 = add2(aq2, q);
@@ -471,20 +472,23 @@ __global__ void __launch_bounds__(L::kThreads, L::kBackward) muon_layer_norm_bac
     row_sums<L, 2>(sum, red, turn);
     if (t == 0 && last >= 0 && r + (p.stages - 1) * step < p.rows) request(last, r + (p.stages - 1) * step);
     if (p.dx.p != nullptr) {
-      // dx = q rstd - rstd aq - h (rstd aqh)
-      const F2 c0 = pair(-rstd * (sum[0] * inv)), c1 = pair(-rstd * (sum[1] * inv));
+      // dx = (q - aq - (x - mean) (rstd aqh)) rstd + skip
+      const F2 c0 = pair(-sum[0] * inv), c1 = pair(-rstd * (sum[1] * inv));
 #pragma unroll
       for (int k = 0; k < L::NV; ++k) {
         F2 x[4], dy[4];
         staged_group<L>(xrow, L::BF16, k, t, p.cols, x);
         staged_group<L>(dyrow, L::BF16, k, t, p.cols, dy);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = fma2(mul2(dy[j], gain[k][j]), scale, fma2(fma2(x[j], scale, shift), c1, c0));
+        for (int j = 0; j < 4; ++j) x[j] = fma2(dy[j], gain[k][j], fma2(add2(x[j], shift), c1, c0));
         if (skip_bytes) {
           const uint8_t* skip = ring.stage(s) + 2 * slot + within_unit<L>(row_address(p.skip, r));
           staged_group<L>(skip, p.skip.bf16, k, t, p.cols, dy);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = add2(x[j], dy[j]);
+          for (int j = 0; j < 4; ++j) x[j] = fma2(x[j], scale, dy[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], scale);
         }
         store_group<L, L::BF16>(p.dx, r * p.dx.ld, k, t, p.cols, x);
       }

@@ -111,3 +111,43 @@ def test_a_workspace_elsewhere_is_refused():
             for call in calls(ws):
                 call()
         assert ws.buf.device == x.device
+
+
+# (a bf16 row 1e4 standard deviations from zero has no two different values, and no rstd)
+FAR = [(64, 768, 1000.0), (37, 1023, 1000.0), (3, 8192, 1000.0), (2, 16400, 1000.0), (50, 257, 0.0)]
+
+
+@pytest.mark.parametrize("rows,cols,far,dtype", [(*c, d) for c in FAR for d in ("f32", "bf16")]
+                         + [(40, 4096, 1e4, "f32")])
+def test_norm_gradients_far_from_zero(rows, cols, far, dtype):
+    """A mean of `far` standard deviations costs the gradients nothing: x - mean is formed first,
+    where it rounds once, relative to itself.
+
+    With u = 2^-24 and h = (x - mean) rstd: |error of h| <= 2 u |h|.  dgain: a column's sum takes
+    at most rows + 8 additions.  dx = rstd (q - avg q - h avg(q h)): q, each average (in
+    n = D / 256 + 44 additions at most) and the three operations that join them."""
+    require_gpu()
+    from newton_schulz_11_b200 import api
+
+    gen = torch.Generator().manual_seed(rows + cols)
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    half = {"f32": U, "bf16": 2.0 ** -8}[dtype]
+    spread = 1.0 if dtype == "f32" else max(1.0, far / 16)
+    x = (torch.randn(rows, cols, generator=gen) * spread + far * spread).to(dt).cuda()
+    dy = (torch.randn(rows, cols, generator=gen) * 0.1).to(dt).cuda()
+    gain = (torch.randn(cols, generator=gen) * 0.3 + 1).cuda()
+    X, G, Q = f64(x), f64(gain), f64(dy) * f64(gain)
+    mean = torch.from_numpy(X.mean(1)).float().cuda()
+    rstd = torch.from_numpy(1 / X.std(1)).float().cuda()
+    dx, dg, db = api.layer_norm_backward(dy, x, mean, rstd, gain)
+    rdx, rdg, rdb = lo.layer_norm_backward(f64(dy), X, f64(mean), f64(rstd), G)
+    r = f64(rstd)[:, None]
+    h = np.abs(X - f64(mean)[:, None]) * r
+    q = np.abs(Q)
+    n = cols / 256 + 44
+    aq, aqh = q.mean(1, keepdims=True), (q * h).mean(1, keepdims=True)
+    t_dx = U * r * (6 * (q + aq + h * aqh) + n * aq + (n + 4) * h * aqh) + (half + U) * np.abs(rdx)
+    assert (np.abs(f64(dx) - rdx) <= t_dx + 1e-38).all(), "dx"
+    t_dg = (rows + 8 + 3) * U * (np.abs(f64(dy)) * h).sum(0)
+    assert (np.abs(f64(dg) - rdg) <= t_dg + 1e-38).all(), "dgain"
+    assert (np.abs(f64(db) - rdb) <= (rows + 8) * U * np.abs(f64(dy)).sum(0) + 1e-38).all(), "dbias"
