@@ -311,8 +311,9 @@ muon_status_t muon_newton_schulz_static(const muon_matrix_t* mats, int n, int ns
  * Numerics: statistics, sums over rows and reductions of products are carried in fp32 (long
  * reductions in pieces whose fp32 sums are added with rounding to nearest).  A bf16 operand
  * of a product goes to the tensor cores as it is; an fp32 one as three bf16 terms that hold
- * all of its 24 bits, so fp32 operands are not rounded (an infinite fp32 operand may give
- * NaN where the exact result is infinite).  Each output is rounded once, to its dtype.
+ * all of its 24 bits, so fp32 operands are not rounded.  An infinity gives the infinity or the
+ * NaN that the exact sum gives (one that meets an fp32 value below 2^-66, which has not all
+ * three terms, may give NaN).  Each output is rounded once, to its dtype.
  * Results do not depend on the order in which blocks run: no atomics on data.
  *
  * Execution, ownership and errors are those of the header's opening comment, with two

@@ -955,41 +955,38 @@ __device__ __forceinline__ void run_sweep(const Sweep& s, int b, F&& f) {
 
 // x = h + m + l: each term takes the leading 8 bits of what is left, truncated, so the three
 // hold the 24 bits of an fp32 value exactly and none overflows (only terms below 2^-133 are
-// lost).  What is not finite goes into h alone.  A bf16 source is copied to rows that TMA can read.
+// lost).  A bf16 source is copied to rows that TMA can read.
+// An infinity in one operand meets every term of the other: inf * 0 of an absent m or l would
+// make the sum NaN.  So a term that nothing is left for is 2^-60 of the value, which no finite
+// sum shows, and an infinity goes into all three: then every term product has the sign of the
+// whole one.
 // Bound by HBM for large operands and by the launch for small ones: 4 bytes read and 6 written
-// an element, about 2 us of the 12.3 of both gradients of 256 x 768 x 768.  Testing for what is
-// not finite once for eight elements, and two rows at a time, took x W^T of 4096 x 1024 x 1024 in
-// fp32 from 56 to 47 us and both gradients of 1000 x 1000 x 1000 from 42.5 to 37.
+// an element, about 2 us of the 12.3 of both gradients of 256 x 768 x 768.  Testing for NaN once
+// for eight elements, and two rows at a time, took x W^T of 4096 x 1024 x 1024 in fp32 from 56
+// to 47 us and both gradients of 1000 x 1000 x 1000 from 42.5 to 37.
 __device__ __forceinline__ void pack_terms(const PackTask& p, int64_t at, float (&x)[8]) {
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-  const bool finite = top < 0x7F800000u;  // all eight: then a term is a few instructions a pair
-  for (int t = 0; t < p.terms; ++t) {
+  if (top > 0x7F800000u) {  // a NaN stays one without its low half
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (isnan(x[j])) x[j] = __uint_as_float(0x7FC00000u);
+  }
+  float least[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) least[j] = fabsf(x[j]) * 0x1p-60f;
+  for (int t = 0;;) {
     uint32_t w[4];
-    if (finite) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a = __float_as_uint(x[2 * j]), b = __float_as_uint(x[2 * j + 1]);
-        w[j] = __byte_perm(a, b, 0x7632);
-        x[2 * j] -= __uint_as_float(a & 0xFFFF0000u);
-        x[2 * j + 1] -= __uint_as_float(b & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(x[j]);
-        uint32_t hi = b >> 16;
-        if ((b & 0x7F800000u) == 0x7F800000u) {
-          if (b & 0x007FFFFFu) hi |= 0x40u;  // a NaN stays one
-          x[j] = 0.f;
-        } else {
-          x[j] -= __uint_as_float(b & 0xFFFF0000u);
-        }
-        w[j >> 1] = (j & 1) ? (w[j >> 1] | (hi << 16)) : hi;
-      }
-    }
+    for (int j = 0; j < 4; ++j) w[j] = __byte_perm(__float_as_uint(x[2 * j]), __float_as_uint(x[2 * j + 1]), 0x7632);
     *reinterpret_cast<uint4*>(p.dst + t * p.term_stride + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (++t == p.terms) break;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // (an infinity leaves NaN, of which and infinity the larger is infinity)
+      const float h = __uint_as_float(__float_as_uint(x[j]) & 0xFFFF0000u);
+      x[j] = copysignf(fmaxf(fabsf(x[j] - h), least[j]), h);
+    }
   }
 }
 

@@ -151,3 +151,69 @@ def test_norm_gradients_far_from_zero(rows, cols, far, dtype):
     t_dg = (rows + 8 + 3) * U * (np.abs(f64(dy)) * h).sum(0)
     assert (np.abs(f64(dg) - rdg) <= t_dg + 1e-38).all(), "dgain"
     assert (np.abs(f64(db) - rdb) <= (rows + 8) * U * np.abs(f64(dy)).sum(0) + 1e-38).all(), "dbias"
+
+
+MIXED = [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16"), ("bf16", "bf16")]
+# few tokens, small products (one CTA a tile, and clusters), pairs, pairs with a split
+# reduction, and outputs whose rows are not 16-byte aligned
+SIZES = [(3, 520, 264), (130, 200, 72), (300, 2000, 264), (2400, 512, 2304), (512, 8192, 512), (301, 203, 261),
+         (2401, 515, 2305)]
+
+
+@pytest.mark.parametrize("xt,wt", MIXED)
+@pytest.mark.parametrize("rows,n_in,n_out", SIZES)
+def test_infinities_meet_every_term(rows, n_in, n_out, xt, wt):
+    """An infinite operand gives infinities and NaNs exactly where the sum in 64 bits has them:
+    against values that are one bf16 term, values that are two or three, and zeros."""
+    require_gpu()
+    from newton_schulz_11_b200 import api
+
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}
+    gen = torch.Generator(device="cuda").manual_seed(rows + n_in)
+    inf = float("inf")
+
+    def mk(r, c, dtype):
+        t = torch.randn(r, c, generator=gen, device="cuda")
+        pick = torch.rand(r, c, generator=gen, device="cuda")
+        t = torch.where(pick < 0.4, t.bfloat16().float(), t)               # one term
+        t = torch.where(pick < 0.2, t.sign() * (1 + 2.0 ** -9), t)         # two
+        t = torch.where(pick < 0.1, t.sign() * 2.0 ** -70, t)
+        t = torch.where(pick < 0.05, torch.zeros_like(t), t)
+        return t.to(dt[dtype])
+
+    def same(got, want, what):
+        got = got.double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+        assert torch.equal(got == inf, want == inf) and torch.equal(got == -inf, want == -inf), what
+
+    x, w, dy = mk(rows, n_in, xt), mk(n_out, n_in, wt), mk(rows, n_out, xt)
+    x[0, 5], x[rows // 2, n_in - 1], w[n_out // 3, 17] = inf, -inf, inf
+    x[rows - 1, 3], x[rows - 1, 170] = inf, -inf
+    out = torch.empty(rows, n_out, device="cuda")
+    same(api.linear(x, w, out=out), x.double() @ w.double().t(), "y")
+    same(api.linear(x, w), x.double() @ w.double().t(), "y in the dtype of x")
+    dy[rows // 3, 2] = -inf
+    dx, dw, db = api.linear_backward(dy, x, w)
+    same(dx, dy.double() @ w.double(), "dx")
+    same(dw, dy.double().t() @ x.double(), "dw")
+    same(db, dy.double().sum(0), "db")
+
+
+@pytest.mark.parametrize("xt,wt", MIXED)
+@pytest.mark.parametrize("rows,n_in,n_out", SIZES)
+def test_whole_numbers_stay_exact(rows, n_in, n_out, xt, wt):
+    """Products of whole numbers below 2^8 (one bf16 term each) whose every partial sum is below
+    2^24 have nothing to round or to truncate, and the terms that stand for nothing add 2^-59 to
+    the sum, far below its half step."""
+    require_gpu()
+    from newton_schulz_11_b200 import api
+
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x, w, dy = (torch.randint(-31, 32, s, generator=gen, device="cuda").to(dt[t])
+                for s, t in (((rows, n_in), xt), ((n_out, n_in), wt), ((rows, n_out), xt)))
+    y, dx = torch.empty(rows, n_out, device="cuda"), torch.empty(rows, n_in, device="cuda")
+    _, dw, db = api.linear_backward(dy, x, w, dx=dx)
+    for got, want in ((api.linear(x, w, out=y), x.double() @ w.double().t()), (dx, dy.double() @ w.double()),
+                      (dw, dy.double().t() @ x.double()), (db, dy.double().sum(0))):
+        assert torch.equal(got.double(), want)
