@@ -240,34 +240,45 @@ PyObject* layer_norm(PyObject* const* a) {
   return pack3(y, mean, rstd);
 }
 
-// (dy, x, mean, rstd, gain, skip, dx, dgain, dbias, accumulate, workspace) -> (dx, dgain, dbias)
+// (dy, x, mean, rstd, gain, skip, dx, dgain, dbias, need_dx, need_dgain, need_dbias, accumulate, workspace)
+// -> (dx, dgain, dbias)
 PyObject* layer_norm_backward(PyObject* const* a) {
   const at::Tensor& x = first(a[1], "x");
   const int64_t rows = x.size(0), cols = x.size(1);
   const c10::Device device = x.device();
   const c10::cuda::CUDAGuard guard(device);
+  const bool need_dx = truth(a[9]), need_dgain = truth(a[10]), need_dbias = truth(a[11]);
   muon_layer_norm_grad_t d{};
-  d.accumulate = truth(a[9]) ? 1 : 0;
-  if (d.accumulate && !(given(a[7]) && given(a[8]))) refuse(PyExc_ValueError, "accumulate needs dgain and dbias");
+  d.accumulate = truth(a[12]) ? 1 : 0;
+  if (d.accumulate && ((need_dgain && !given(a[7])) || (need_dbias && !given(a[8]))))
+    refuse(PyExc_ValueError, "accumulate needs dgain and dbias");
+  if (!(need_dx || need_dgain || need_dbias)) refuse(PyExc_ValueError, "nothing to compute");
   const at::ScalarType xt = x.scalar_type();
   d.x = matrix(x, "x", rows, cols, device);
   d.dy = matrix(tensor(a[0], "dy"), "dy", rows, cols, device, xt);
   d.mean = f32_vector(tensor(a[2], "mean"), "mean", rows, device);
   d.rstd = f32_vector(tensor(a[3], "rstd"), "rstd", rows, device);
   d.gain = vector_or_absent(a[4], "gain", cols, device);
-  d.skip = matrix_or_absent(a[5], "skip", rows, cols, device);
-  const at::Tensor dx = output(a[6], "dx", {rows, cols}, xt, device);
-  const at::Tensor dgain = output(a[7], "dgain", {cols}, at::kFloat, device);
-  const at::Tensor dbias = output(a[8], "dbias", {cols}, at::kFloat, device);
-  d.dx = matrix(dx, "dx", rows, cols, device, xt);
-  d.dgain = f32_vector(dgain, "dgain", cols, device);
-  d.dbias = f32_vector(dbias, "dbias", cols, device);
+  at::Tensor dx, dgain, dbias;
+  if (need_dx) {
+    dx = output(a[6], "dx", {rows, cols}, xt, device);
+    d.dx = matrix(dx, "dx", rows, cols, device, xt);
+    d.skip = matrix_or_absent(a[5], "skip", rows, cols, device);
+  }
+  if (need_dgain) {
+    dgain = output(a[7], "dgain", {cols}, at::kFloat, device);
+    d.dgain = f32_vector(dgain, "dgain", cols, device);
+  }
+  if (need_dbias) {
+    dbias = output(a[8], "dbias", {cols}, at::kFloat, device);
+    d.dbias = f32_vector(dbias, "dbias", cols, device);
+  }
   d.rows = rows;
   d.cols = cols;
   void* stream = current_stream(device);
   size_t need = 0;
   check(muon_layer_norm_backward_workspace(&d, &need), "muon_layer_norm_backward");
-  const Scratch ws(need, a[10], device, stream);
+  const Scratch ws(need, a[13], device, stream);
   check(muon_layer_norm_backward(&d, ws.ptr, ws.bytes, stream), "muon_layer_norm_backward");
   return pack3(dx, dgain, dbias);
 }
@@ -402,7 +413,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {
     method<layer_norm, 5>("layer_norm"),
-    method<layer_norm_backward, 11>("layer_norm_backward"),
+    method<layer_norm_backward, 14>("layer_norm_backward"),
     method<linear, 9>("linear"),
     method<linear_backward, 14>("linear_backward"),
     method<activation_backward, 4>("activation_backward"),

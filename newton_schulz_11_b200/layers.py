@@ -78,20 +78,23 @@ def layer_norm(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias: Optio
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                         gain: Optional[torch.Tensor] = None, *, skip: Optional[torch.Tensor] = None,
                         dx: Optional[torch.Tensor] = None, dgain: Optional[torch.Tensor] = None,
-                        dbias: Optional[torch.Tensor] = None, accumulate: bool = False, workspace=None,
-                        stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    """Gradients of layer_norm: (dx, dgain, dbias).
+                        dbias: Optional[torch.Tensor] = None, need_dx: bool = True, need_dgain: bool = True,
+                        need_dbias: bool = True, accumulate: bool = False, workspace=None, stream=None):
+    """Gradients of layer_norm: (dx, dgain, dbias), None where not needed.
 
     dy and dx have x's dtype; mean and rstd are what layer_norm returned.  `skip` (fp32 or
     bf16) is added to dx: the gradient that the residual connection around the norm carries;
     dx may be the same tensor.  dgain and dbias are fp32 [width] (allocated when None); with
-    `accumulate` they must be given and the gradients are added to them.
+    `accumulate` those that are needed must be given and the gradients are added to them.  A
+    norm without a bias has need_dbias=False.
     """
     if stream is not None:
         with _on(stream, x):
             return layer_norm_backward(dy, x, mean, rstd, gain, skip=skip, dx=dx, dgain=dgain, dbias=dbias,
+                                       need_dx=need_dx, need_dgain=need_dgain, need_dbias=need_dbias,
                                        accumulate=accumulate, workspace=workspace)
-    return _ops().layer_norm_backward(dy, x, mean, rstd, gain, skip, dx, dgain, dbias, accumulate, workspace)
+    return _ops().layer_norm_backward(dy, x, mean, rstd, gain, skip, dx, dgain, dbias, need_dx, need_dgain, need_dbias,
+                                      accumulate, workspace)
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *, act: Optional[str] = None,

@@ -217,3 +217,28 @@ def test_whole_numbers_stay_exact(rows, n_in, n_out, xt, wt):
     for got, want in ((api.linear(x, w, out=y), x.double() @ w.double().t()), (dx, dy.double() @ w.double()),
                       (dw, dy.double().t() @ x.double()), (db, dy.double().sum(0))):
         assert torch.equal(got.double(), want)
+
+
+@pytest.mark.parametrize("rows,cols", [(50, 768), (20, 1023), (9, 9000), (0, 64)])
+def test_norm_gradients_that_are_asked_for(rows, cols):
+    """Each alone and in pairs, and a norm without a bias that accumulates its gain's gradient."""
+    require_gpu()
+    from newton_schulz_11_b200 import api
+
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x, dy, skip = (torch.randn(rows, cols, generator=gen, device="cuda") for _ in range(3))
+    _, mean, rstd = api.layer_norm(x)
+    names = ("need_dx", "need_dgain", "need_dbias")
+    want = api.layer_norm_backward(dy, x, mean, rstd, skip=skip)
+    for mask in range(1, 8):
+        need = {n: bool(mask >> i & 1) for i, n in enumerate(names)}
+        got = api.layer_norm_backward(dy, x, mean, rstd, skip=skip, **need)
+        for i, n in enumerate(names):
+            assert torch.equal(got[i], want[i]) if need[n] else got[i] is None
+    for i, (kw, no) in enumerate(((dict(dgain=want[1].clone()), "need_dbias"), (dict(dbias=want[2].clone()), "need_dgain"))):
+        got = api.layer_norm_backward(dy, x, mean, rstd, accumulate=True, **{no: False}, **kw)
+        assert got[2 - i] is None and torch.equal(got[1 + i], want[1 + i] + want[1 + i])
+        with pytest.raises(ValueError, match="accumulate needs"):
+            api.layer_norm_backward(dy, x, mean, rstd, accumulate=True, **kw)
+    with pytest.raises(ValueError, match="nothing to compute"):
+        api.layer_norm_backward(dy, x, mean, rstd, **dict.fromkeys(names, False))
