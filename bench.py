@@ -1221,7 +1221,7 @@ def mlp_config(w, layers, world):
 def run_mlp(args, world, rank, local):
     import torch
 
-    from newton_schulz_11_b200 import api, build
+    from newton_schulz_11_b200 import _lib, api, build
 
     build.build()
     torch.cuda.set_device(local)
@@ -1249,7 +1249,9 @@ def run_mlp(args, world, rank, local):
     clocks = Clocks(local)
     clocks.start()
     clocks.mark(True)
+    launches = _lib.lib().muon_launch_count()
     ms_step = timed(args.steps, lambda: step(stream))
+    launches = _lib.lib().muon_launch_count() - launches
     clocks.mark(False)
     clk = clocks.stop()
     ms_layers = timed(max(1, min(args.steps, 20)), step.layers_pass)
@@ -1283,8 +1285,7 @@ def run_mlp(args, world, rank, local):
         "optimizer": {"ms": round(ms_step - ms_layers, 4), "newton_schulz_tflops":
                       round(ns / max(ms_step - ms_layers, 1e-6) / 1e9, 1)},
         "clocks": clk, "e2e": e2e,
-        # at least: a norm, two products and their four gradients' products, the norm's two a block
-        "gpu_launches": (9 * len(layers) + 1) * args.steps,
+        "gpu_launches": launches,
     }
     if world == 1 and not args.no_cpu_baseline:
         cms, sample = mlp_oracle_ms(w, layers, MLP_TOKENS)

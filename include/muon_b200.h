@@ -199,6 +199,12 @@ muon_status_t muon_nonfinite_count(const void* workspace, void* stream, int64_t*
 muon_status_t muon_set_wait_timeout_us(int64_t us);
 
 /*
+ * Kernel launches that the library's entry points have queued in this process, of every kind
+ * and on every stream.  A captured call counts once, at its capture; replays are not seen.
+ */
+int64_t muon_launch_count(void);
+
+/*
  * Per-kernel timing for diagnostics and benchmarks.  Between muon_profile_begin and
  * muon_profile_end every launch the library queues is bracketed by a pair of CUDA
  * events recorded on its own stream (the Muon step's kernels only: the layer entry points

@@ -51,6 +51,7 @@ EXPORTS = (
     "muon_linear_backward_workspace",
     "muon_activation_backward",
     "muon_layers_status",
+    "muon_launch_count",
 )
 
 KIND_NAMES = ("momentum", "norm", "gram", "poly", "apply", "apply_last")
@@ -248,6 +249,8 @@ def lib() -> ctypes.CDLL:
             f.argtypes = [P(desc), ctypes.c_void_p]
         h.muon_layers_status.restype = ctypes.c_int
         h.muon_layers_status.argtypes = [ctypes.c_void_p, ctypes.c_int, P(ctypes.c_int32), P(ctypes.c_int32)]
+        h.muon_launch_count.restype = ctypes.c_int64
+        h.muon_launch_count.argtypes = []
         _lib = h
         return h
 

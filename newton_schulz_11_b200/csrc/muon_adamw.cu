@@ -19,6 +19,7 @@
 
 #include "muon_b200.h"
 #include "muon_device.cuh"
+#include "muon_params.h"
 
 namespace muon {
 
@@ -258,7 +259,7 @@ extern "C" muon_status_t muon_adamw_step(const muon_adamw_tensor_t* ts, int n, f
     a.n = cnt;
     if (chunks > 0x7fffffff) return MUON_ERR_UNSUPPORTED_SHAPE;
     muon::muon_adamw_kernel<<<static_cast<unsigned>(chunks), muon::kAdamThreads, 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    if (muon::counted(cudaGetLastError()) != cudaSuccess) return MUON_ERR_CUDA;
   }
   return MUON_OK;
 }

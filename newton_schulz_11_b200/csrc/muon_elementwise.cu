@@ -206,7 +206,7 @@ static cudaError_t launch_pdl(K kernel, int grid, const EwParams& p, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return counted(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 cudaError_t launch_momentum(const EwParams& p, cudaStream_t stream) {

@@ -44,6 +44,7 @@ constexpr int64_t kChunkElems = 16384;
 constexpr int kStagedApplyMaxM = 1024;  // Gram side up to which the staged (64-deep) variants serve
 
 std::atomic<long long> g_timeout_us{2000000};
+std::atomic<long long> g_launches{0};
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
@@ -712,6 +713,11 @@ muon_status_t run(const muon_matrix_t* mats, int n, float lr, float beta, float 
 
 }  // namespace
 
+cudaError_t muon::counted(cudaError_t e) {
+  if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
+  return e;
+}
+
 // What the layer entry points share with the step: device facts and the wait budget.
 muon_status_t muon::layers_device(int* sms) {
   int dev = 0;
@@ -852,6 +858,8 @@ muon_status_t muon_set_wait_timeout_us(int64_t us) {
   g_timeout_us.store(us > 0 ? us : 2000000);
   return MUON_OK;
 }
+
+int64_t muon_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 muon_status_t muon_profile_begin(void) {
   g_prof.on = true;

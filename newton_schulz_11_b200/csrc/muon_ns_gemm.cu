@@ -1224,7 +1224,7 @@ static cudaError_t launch_one(const typename ParamsOf<MODE>::type& p, int max_pa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return counted(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 int gemm_tile_rows() { return 256; }

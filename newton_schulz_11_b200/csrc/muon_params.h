@@ -7,9 +7,13 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace muon {
+
+// `e`, the outcome of a kernel launch; one that was queued is counted (muon_launch_count).
+cudaError_t counted(cudaError_t e);
 
 constexpr int kMaxClasses = 8;      // distinct shapes per wave
 constexpr int kMaxWaveMats = 128;   // matrices per wave

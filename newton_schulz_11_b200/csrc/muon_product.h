@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "muon_params.h"
+
 namespace muon {
 
 // One operand of the epilogue.  vec: rows may be accessed 32 (2) or 16 (1) bytes at a time
@@ -177,7 +179,7 @@ cudaError_t launch_dependent(K kernel, const P& p, dim3 grid, int threads, cudaS
   attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return counted(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 }  // namespace muon
