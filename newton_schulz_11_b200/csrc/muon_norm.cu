@@ -184,8 +184,8 @@ __device__ __forceinline__ void join_groups(F2 (*d)[4], F2* own, int group, int 
 // Bound by HBM where rows are long, by the issue of the row sums' instructions where a warp has
 // a short row, by the launch for few rows.  Captured calls (us, and of the measured copy
 // bandwidth): forward bf16 32768 x 4096 91.4 (91%), 32768 x 768 18.0 (87%), 8 x 768 3.1; backward
-// bf16 32768 x 4096 129 (97%), 16384 x 768 24.5 (64%, with the join of its parameter gradients),
-// fp32 1001 x 1023 with unaligned rows 9.3.
+// bf16 32768 x 4096 130 (96%), 16384 x 768 24.2 (65%, with the join of its parameter gradients),
+// fp32 1001 x 1023 with unaligned rows 9.5.
 //
 // A copy that does not land within the budget is recorded in the status word; the group
 // then carries on without waiting, so that every barrier is still met, and leaves.
@@ -797,10 +797,13 @@ extern "C" muon_status_t muon_layer_norm(const muon_layer_norm_t* d, void* strea
                                    dim3(static_cast<unsigned>(row_blocks(d->rows, 1, 4))), kWideThreads, s));
   const bool vec = whole_groups(d->cols, {&p.x, &p.y, &p.gain, &p.bias}), bf16 = p.x.bf16 != 0;
   return with_shape(d->cols, [&](auto t, auto n) {
-    // Forward, the checks for missing columns cost instructions where a warp or a wide block
-    // has the row, and help where they happen to space its accesses (us, with and without, at
-    // 134 M elements or 32768 rows): bf16 768 19.4, 18.2; 2048 50, 53; 4096 91, 100; 8192 110,
-    // 107; fp32 1024 51, 54; 4096 100, 95.  (Backward they always cost: 4096 bf16 149, 131.)
+    // Forward, the checks for missing columns cost instructions but some shapes are quicker with
+    // them; why is not known.  At 2^27 bf16 elements, us with and without: 256 columns 125, 111;
+    // 512 99, 106; 768 104, 103; 1024 105, 101; 2048 101, 105; 4096 91, 101; 6144 96, 99; 8192
+    // 110, 107.  At 2^26 fp32 elements: 256 104, 102; 512 102, 103; 768 93, 105; 1024 98, 107;
+    // 2048 95, 97; 4096 101, 95; 6144 104, 102; 8192 111, 108.  So a warp's row and the widest
+    // leave them out in bf16, a block's row in fp32 (bf16 512 and fp32 2048 lose 7% and 2% by
+    // that).  Backward they always cost: 4096 bf16 149, 131.
     constexpr bool wide32 = t() >= 128, full16 = t() == 32 || t() == 512;
     const bool full = d->cols == t() * n() * 8;
     if (vec && full && bf16 && full16) return run_norm<t(), n(), true, full16 ? kFull : kGroups8>(p, s);
