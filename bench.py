@@ -81,6 +81,8 @@ def kernel_source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "newton_schulz_11_b200", "csrc")
     for name in sorted(os.listdir(csrc)):
+        if not os.path.isfile(os.path.join(csrc, name)):
+            continue
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             h.update(name.encode() + _code_only(f.read()).encode())
     return h.hexdigest()[:16]

@@ -81,3 +81,16 @@ def test_benchmark_reports_the_launches_of_its_steps():
     step(torch.cuda.current_stream())
     torch.cuda.synchronize()
     assert line["gpu_launches"] == 3 * (lib.muon_launch_count() - before)
+
+
+def test_source_hash_reads_files_only(tmp_path, monkeypatch):
+    """A cache folder that a tool left among the sources does not end the benchmark."""
+    import bench
+
+    csrc = tmp_path / "newton_schulz_11_b200" / "csrc"
+    csrc.mkdir(parents=True)
+    (csrc / "a.cu").write_text("int a;")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    h = bench.kernel_source_hash()
+    (csrc / ".cache").mkdir()
+    assert bench.kernel_source_hash() == h
